@@ -264,6 +264,66 @@ mr_status cast_f32_bf16(const float *X, int64_t ldx, void *Y, int64_t ldy, int32
                         void *stream);
 
 /*
+ * 4-bit weights with group scales
+ * -------------------------------
+ * A weight row j is k values q in 0..15; every group of G consecutive k has
+ * a scale s and, optionally, a zero point z in 0..15 (8 without).  The weight
+ * it stands for is (q - z) * s.  The kernels read it in a packed order that
+ * w4_pack writes once, when a weight is loaded.
+ *
+ * A format is a uint32: the group size (32, 64 or 128), plus MR_W4_ZEROS when
+ * there are zero points, plus MR_W4_SCALE_F16 when the scales are f16 (bf16
+ * without).  k is a multiple of G.
+ *
+ * The packed order: tiles of 16 weight rows; a tile's k in blocks of 128, one
+ * after the other (the last one padded with zero weight, and rows past n
+ * too); a block is 1024 bytes of values, then the scales [128 / G][16 rows],
+ * then the zero points [128 / G][16 rows], one byte each.  Value bytes: for
+ * half h = 0, 1 and l = 4g + t = 0..31, four 32-bit words of row 8h + g, word
+ * j holding k = 32j + 8t .. + 7: nibble i is value 2i, nibble 4 + i is value
+ * 2i + 1.  With `paired` the rows are two halves of equal length (a gate and
+ * an up projection), and tile T holds rows 8T .. 8T + 7 of either half.
+ */
+#define MR_W4_GROUP_MASK 0xFFu
+#define MR_W4_ZEROS 0x100u
+#define MR_W4_SCALE_F16 0x200u
+
+/* Bytes of one packed n x k weight (0 for invalid sizes or formats). */
+size_t w4_packed_bytes(int32_t n, int32_t k, uint32_t fmt, int32_t paired);
+
+/*
+ * w4_pack -- lay out `count` weights of n x k for mrgemv_w4 / moe_window_w4.
+ *
+ * q      : [count][n][k / 2] bytes, value 2i of a row in the low half of byte
+ *          i and value 2i + 1 in the high half; 4-byte aligned, contiguous.
+ * scales : [count][n][k / G] bf16 (f16 with MR_W4_SCALE_F16), contiguous.
+ * zeros  : [count][n][k / G] bytes (low 4 bits used) with MR_W4_ZEROS, else NULL.
+ * packed : count * w4_packed_bytes(n, k, fmt, paired) bytes, 16-byte aligned.
+ * k % G == 0; with `paired`, n is even.  A group size other than 32, 64 and
+ * 128 is MR_ERR_UNSUPPORTED.
+ */
+mr_status w4_pack(const void *q, const void *scales, const void *zeros, void *packed, size_t packed_bytes,
+                  int32_t count, int32_t n, int32_t k, uint32_t fmt, int32_t paired, void *stream);
+
+/*
+ * mrgemv_w4 -- mrgemv_bf16 with a 4-bit weight:
+ *
+ *   C[i][j] = sum_grp s[j][grp] * sum_{p in grp} A[i][p] * (q[j][p] - z[j][grp])
+ *
+ * A      : m rows of k values of in_dtype (MR_BF16 or MR_F16), row stride lda.
+ * packed : the weight as w4_pack wrote it (unpaired), packed_bytes long.
+ * C      : m rows of n fp32, row stride ldc (>= n), device (written).
+ * 1 <= m <= 16; lda % 8 == 0; A and packed 16-byte aligned.  A is held in
+ * shared memory: k <= 4096 is always accepted, more where m rows of it fit
+ * (MR_ERR_UNSUPPORTED otherwise).  flags: 0 or MR_GEMV_PDL.
+ * Sums are fp32: groups on the tensor core, their scaled sums in k order.  Row
+ * i's result is bitwise identical for every m and every position of the row.
+ */
+mr_status mrgemv_w4(const void *A, int64_t lda, const void *packed, size_t packed_bytes, float *C,
+                    int64_t ldc, int32_t m, int32_t n, int32_t k, int32_t in_dtype, uint32_t fmt,
+                    uint32_t flags, void *stream);
+
+/*
  * gemm_f16 -- tiled GEMM on the tcgen05 tensor cores (TMA -> shared memory
  * -> tcgen05.mma with the accumulator in tensor memory), fp32 accumulate.
  *

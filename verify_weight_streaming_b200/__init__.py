@@ -19,6 +19,7 @@ MR_F16, MR_BF16, MR_F32 = 0, 1, 2
 MR_GEMV_PDL = 0x1
 MR_GEMV_SIGMOID = 0x2
 MR_ROUTER_TWO_LAUNCH = 0x4
+MR_W4_GROUP_MASK, MR_W4_ZEROS, MR_W4_SCALE_F16 = 0xFF, 0x100, 0x200
 MR_DEVERR_GEMV_TIMEOUT, MR_DEVERR_GEMM_TIMEOUT, MR_DEVERR_TOPK_TIMEOUT, MR_DEVERR_SELFTEST = 1, 2, 4, 8
 
 EXPORTS = (
@@ -27,7 +28,7 @@ EXPORTS = (
     "router_gemv_topk_workspace_bytes", "router_gemv_topk_noalloc", "router_gemv_topk_noalloc_max_logits", "gemm_f16_grouped",
     "gemm_f16_grouped_select_tile", "cast_f32_bf16", "gemm_f16_ex", "gemm_f16", "gemm_f16_num_tiles",
     "gemm_f16_tile_name", "gemm_f16_select_tile", "mr_poll_errors", "mr_selftest_wait_timeout",
-    "mr_status_str", "mr_version",
+    "mr_status_str", "mr_version", "w4_packed_bytes", "w4_pack", "mrgemv_w4",
 )
 
 
@@ -76,6 +77,12 @@ def _load() -> ctypes.CDLL:
     L.mr_status_str.restype = ctypes.c_char_p
     L.mr_version.argtypes = []
     L.mr_version.restype = ctypes.c_char_p
+    L.w4_packed_bytes.argtypes = [I32, I32, U32, I32]
+    L.w4_packed_bytes.restype = ctypes.c_size_t
+    L.w4_pack.argtypes = [P, P, P, P, ctypes.c_size_t, I32, I32, I32, U32, I32, P]
+    L.mrgemv_w4.argtypes = [P, I64, P, ctypes.c_size_t, P, I64, I32, I32, I32, I32, U32, U32, P]
+    for name in ("w4_pack", "mrgemv_w4"):
+        getattr(L, name).restype = ctypes.c_int
     for name in ("mrgemv_bf16", "mrgemv_bf16_ex", "mrgemv_bf16_plan", "router_topk", "router_topk_ex",
                  "router_topk_merge", "router_gemv_topk",
                  "router_gemv_topk_noalloc", "gemm_f16_grouped", "gemm_f16_grouped_select_tile",
@@ -329,3 +336,48 @@ def mr_poll_errors(stream=None) -> int:
 
 def mr_selftest_wait_timeout(limit_us: int, stream=None) -> None:
     _check(lib.mr_selftest_wait_timeout(limit_us, _stream(stream)), "mr_selftest_wait_timeout")
+
+
+def w4_format(group: int, zeros: bool, scale_dtype) -> int:
+    """The format word of a 4-bit weight: group size, zero points or not, torch.bfloat16 or torch.float16 scales."""
+    import torch
+    if scale_dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("scales must be bfloat16 or float16")
+    return group | (MR_W4_ZEROS if zeros else 0) | (MR_W4_SCALE_F16 if scale_dtype == torch.float16 else 0)
+
+
+def w4_packed_bytes(n: int, k: int, fmt: int, paired: bool = False) -> int:
+    return int(lib.w4_packed_bytes(n, k, fmt, 1 if paired else 0))
+
+
+def w4_pack(q, scales, zeros, packed, paired: bool = False, stream=None) -> None:
+    """packed (uint8) = the weights q[..., n, k/2] (uint8, low half first), scales[..., n, k/G] (bf16 or f16) and
+    zeros[..., n, k/G] (uint8, or None) in the order mrgemv_w4 and moe_window_w4 read."""
+    import torch
+    if q.dim() not in (2, 3) or q.dtype != torch.uint8 or packed.dtype != torch.uint8:
+        raise ValueError("q must be uint8 [n, k/2] or [count, n, k/2], packed uint8")
+    n, k = q.shape[-2], 2 * q.shape[-1]
+    count = q.shape[0] if q.dim() == 3 else 1
+    groups = scales.shape[-1]
+    if tuple(scales.shape[:-1]) != tuple(q.shape[:-1]) or groups < 1 or k % groups:
+        raise ValueError("scales must be [..., n, k/G]")
+    if zeros is not None and (zeros.shape != scales.shape or zeros.dtype != torch.uint8):
+        raise ValueError("zeros must be uint8 of the scales' shape")
+    for t in (q, scales, packed) if zeros is None else (q, scales, packed, zeros):
+        if not t.is_contiguous():
+            raise ValueError("q, scales, zeros and packed must be contiguous")
+    fmt = w4_format(k // groups, zeros is not None, scales.dtype)
+    st = lib.w4_pack(q.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(), packed.data_ptr(),
+                     packed.numel(), count, n, k, fmt, 1 if paired else 0, _stream(stream))
+    _check(st, "w4_pack")
+
+
+def mrgemv_w4(A, packed, C, fmt: int, stream=None, flags: int = 0) -> None:
+    """C[m,n] (fp32) = A[m,k] (bf16 or f16) . (the packed 4-bit n x k weight)^T; m <= 16."""
+    m, k, lda = _rows(A, "A")
+    mc, n, ldc = _rows(C, "C")
+    if mc != m:
+        raise ValueError(f"shape mismatch A{tuple(A.shape)} C{tuple(C.shape)}")
+    st = lib.mrgemv_w4(A.data_ptr(), lda, packed.data_ptr(), packed.numel() * packed.element_size(), C.data_ptr(),
+                       ldc, m, n, k, _dtype_code(A), fmt, flags, _stream(stream))
+    _check(st, "mrgemv_w4")

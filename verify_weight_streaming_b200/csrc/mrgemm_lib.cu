@@ -5,3 +5,4 @@
 #include "router_topk.cu"
 #include "gemm_f16.cu"
 #include "cast_bf16.cu"
+#include "mrgemv_w4.cu"

@@ -1,0 +1,179 @@
+// Shared pieces of the kernels that stream a weight past a few activation
+// columns on mma.sync m16n8k16 (mrgemv_w4, moe_window_*).
+//
+// Orientation.  A tile is 16 weight rows (the M of the instruction); the
+// activations of up to 8 tokens are its N columns.  The instruction's k index
+// may be any permutation of the real one as long as both operands use the
+// same: lane l = 4g + t takes, of every 32 consecutive k, the 8 values
+// [8t, 8t + 8) of rows g and g + 8, and the same 8 values of column g.  Those
+// are one 16-byte load per row and column, and they feed two instructions.
+// Nothing is rearranged between memory and the tensor core.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace mr {
+namespace w4 {
+
+constexpr int kTileRows = 16;
+constexpr int kBlockK = 128;        // k values of one packed block
+constexpr int kBlockQ = 1024;       // bytes of a block's 4-bit values
+
+// Bytes of one packed block (16 rows x 128 k) of format `fmt`: the values,
+// 16 scales a group, and 16 zero points a group when the format has them.
+__host__ __device__ inline int block_bytes(uint32_t fmt) {
+    const int groups = kBlockK / (int)(fmt & MR_W4_GROUP_MASK);
+    return kBlockQ + groups * 32 + ((fmt & MR_W4_ZEROS) ? groups * 16 : 0);
+}
+
+// ---- asynchronous copies into the issuing lane's own bytes ----------------
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// 16 bytes of zeros when !valid (nothing is read then).
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool valid) {
+    const int n = valid ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// ---- the matrix instruction -----------------------------------------------
+
+// d += a (16 x 16, row) . b (16 x 8, col), fp32 accumulators.
+template <bool F16>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    if constexpr (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// ---- 4-bit values ---------------------------------------------------------
+
+// One word holds 8 values: nibble i is value 2i, nibble 4 + i is value 2i + 1.
+// Pair i is (q - z) of both, exact: the nibble is put into the low mantissa
+// bits of 128 (bf16) or 1024 (f16), whose spacing is 1 there, and 128 + z or
+// 1024 + z (`zero`, both halves) is subtracted.
+template <bool F16>
+__device__ __forceinline__ uint32_t pair(uint32_t word, int i, uint32_t zero) {
+    const uint32_t v = ((word >> (4 * i)) & 0x000F000Fu) | (F16 ? 0x64006400u : 0x43004300u);
+    uint32_t r;
+    if constexpr (F16)
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(zero));
+    else
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(zero));
+    return r;
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t zero_pair(uint32_t z) {
+    return z * 0x00010001u + (F16 ? 0x64006400u : 0x43004300u);
+}
+
+// A stored 16-bit scale in fp32 (exact).
+__device__ __forceinline__ float scale_value(uint16_t bits, bool f16) {
+    return f16 ? __half2float(__ushort_as_half(bits)) : __uint_as_float((uint32_t)bits << 16);
+}
+
+__device__ __forceinline__ uint16_t lds_u16(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// Request one packed block into `stage` (asynchronous; the caller commits).
+__device__ __forceinline__ void issue_block(uint32_t stage, const uint8_t *src, int bytes, int lane) {
+    cp_async16(stage + 16 * lane, src + 16 * lane);
+    cp_async16(stage + 512 + 16 * lane, src + 512 + 16 * lane);
+    if (kBlockQ + 16 * lane < bytes) cp_async16(stage + kBlockQ + 16 * lane, src + kBlockQ + 16 * lane);
+}
+
+// C += (one packed block) . (the activation columns).  x[c] is the shared
+// address of this lane's 16 bytes of column g of column tile c at the block's
+// first k, on[c] whether that column exists.  The values of a group are
+// summed by the tensor core as small exact integers times the activations
+// and take their scale once, in fp32: the sum of at most 128 products is the
+// longest chain of the matrix instruction's own additions, which round
+// towards zero, so its error does not grow with k.
+template <int G, bool F16, int NT>
+__device__ __forceinline__ void consume_block(uint32_t stage, uint32_t fmt, const uint32_t (&x)[NT],
+                                              const bool (&on)[NT], float (&C)[NT][4], int lane) {
+    const int g = lane >> 2;
+    const uint4 v0 = lds128(stage + 16 * lane), v8 = lds128(stage + 512 + 16 * lane);
+    const uint32_t q0[4] = {v0.x, v0.y, v0.z, v0.w}, q8[4] = {v8.x, v8.y, v8.z, v8.w};
+    const bool sf16 = (fmt & MR_W4_SCALE_F16) != 0, zeros = (fmt & MR_W4_ZEROS) != 0;
+    constexpr int kGroups = kBlockK / G;
+    const uint32_t scales = stage + kBlockQ, zs = scales + 32 * kGroups;
+#pragma unroll
+    for (int gi = 0; gi < kGroups; ++gi) {
+        uint32_t z0 = zero_pair<F16>(8u), z8 = z0;
+        if (zeros) {
+            z0 = zero_pair<F16>(lds_u8(zs + 16 * gi + g));
+            z8 = zero_pair<F16>(lds_u8(zs + 16 * gi + g + 8));
+        }
+        float acc[NT][4] = {};
+#pragma unroll
+        for (int j = gi * (G / 32); j < (gi + 1) * (G / 32); ++j) {
+            uint32_t a0[4], a8[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a0[i] = pair<F16>(q0[j], i, z0);
+                a8[i] = pair<F16>(q8[j], i, z8);
+            }
+#pragma unroll
+            for (int c = 0; c < NT; ++c) {
+                uint4 b = make_uint4(0, 0, 0, 0);
+                if (on[c]) b = lds128(x[c] + 64 * j);
+                mma<F16>(acc[c], a0[0], a8[0], a0[1], a8[1], b.x, b.y);
+                mma<F16>(acc[c], a0[2], a8[2], a0[3], a8[3], b.z, b.w);
+            }
+        }
+        const float s0 = scale_value(lds_u16(scales + 32 * gi + 2 * g), sf16);
+        const float s8 = scale_value(lds_u16(scales + 32 * gi + 2 * g + 16), sf16);
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+            C[c][0] = fmaf(s0, acc[c][0], C[c][0]);
+            C[c][1] = fmaf(s0, acc[c][1], C[c][1]);
+            C[c][2] = fmaf(s8, acc[c][2], C[c][2]);
+            C[c][3] = fmaf(s8, acc[c][3], C[c][3]);
+        }
+    }
+}
+
+}  // namespace w4
+}  // namespace mr
