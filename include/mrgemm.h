@@ -324,6 +324,63 @@ mr_status mrgemv_w4(const void *A, int64_t lda, const void *packed, size_t packe
                     uint32_t flags, void *stream);
 
 /*
+ * moe_window_bf16 / moe_window_w4 -- the routed experts of a verify window:
+ * for the m <= 16 rows and the topk choices router_topk (or router_gemv_topk,
+ * router_topk_merge) made for each,
+ *
+ *   Y[t] = sum_s w[t][s] * Wdown[e] . (silu(G) * U),  e = ids[t][s] - expert_base,
+ *   G, U = the two halves of Wup[e] . X[t]
+ *
+ * X       : m rows of `hidden` bf16, row stride ldx.
+ * ids     : m rows of topk int32, row stride ldr.  An entry outside
+ *           [expert_base, expert_base + experts) adds nothing: -1 marks an
+ *           empty entry, and on a device that holds a part of the experts the
+ *           others' entries are left to them (add the devices' Y).  An expert
+ *           may appear more than once in a row.
+ * weights : m rows of topk fp32 (row stride ldr).  As they are, or with
+ *           MR_MOE_SOFTMAX as logits: w is then their softmax over the row's
+ *           entries with ids >= 0 (held here or not).
+ * Wup     : [experts][2 * inter][hidden] bf16, the gate rows before the up
+ *           rows; row stride ldu, expert stride stride_up, in elements.
+ * Wdown   : [experts][hidden][inter] bf16; row stride ldd, expert stride
+ *           stride_down.
+ * up, down: (w4) the same weights packed by w4_pack with count = experts: up
+ *           paired (n = 2 * inter, k = hidden), down unpaired (n = hidden,
+ *           k = inter), both of format fmt; hidden and inter multiples of G.
+ * Y       : m rows of `hidden` values of out_dtype (MR_F32 or MR_BF16, rounded
+ *           to nearest even once), row stride ldy.  A row with no entry held
+ *           here is zero.
+ * workspace : moe_window_workspace_bytes(m, topk, hidden, inter) bytes of
+ *           device memory, 256-byte aligned; need not be zeroed.  Calls that
+ *           may run at the same time need separate workspaces.
+ * 1 <= m <= 16, 1 <= topk <= 32; hidden, inter, ldx, ldu, ldd and the expert
+ * strides multiples of 8; X and the weights 16-byte aligned.  X is held in
+ * shared memory, and so are up to min(m, 8) rows of the activations: hidden
+ * <= 4096 and inter <= 2048 are always accepted, more where they fit
+ * (MR_ERR_UNSUPPORTED otherwise).
+ * Only experts that some row picked are read, each once (again for every
+ * further 8 rows that picked it).  Products are summed in fp32 and the
+ * activations keep fp32's precision; a row's bits depend on its own X, ids
+ * and weights, not on m or the other rows.
+ */
+#define MR_MOE_SOFTMAX 0x1u
+
+size_t moe_window_workspace_bytes(int32_t m, int32_t topk, int32_t hidden, int32_t inter);
+
+mr_status moe_window_bf16(const void *X, int64_t ldx, const int32_t *ids, const float *weights, int64_t ldr,
+                          const void *Wup, int64_t ldu, int64_t stride_up, const void *Wdown, int64_t ldd,
+                          int64_t stride_down, void *Y, int64_t ldy, int32_t m, int32_t topk,
+                          int32_t experts, int32_t hidden, int32_t inter, int32_t expert_base,
+                          int32_t out_dtype, uint32_t flags, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+mr_status moe_window_w4(const void *X, int64_t ldx, const int32_t *ids, const float *weights, int64_t ldr,
+                        const void *up, size_t up_bytes, const void *down, size_t down_bytes, void *Y,
+                        int64_t ldy, int32_t m, int32_t topk, int32_t experts, int32_t hidden,
+                        int32_t inter, int32_t expert_base, uint32_t fmt, int32_t out_dtype,
+                        uint32_t flags, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * gemm_f16 -- tiled GEMM on the tcgen05 tensor cores (TMA -> shared memory
  * -> tcgen05.mma with the accumulator in tensor memory), fp32 accumulate.
  *

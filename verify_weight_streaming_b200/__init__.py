@@ -20,6 +20,7 @@ MR_GEMV_PDL = 0x1
 MR_GEMV_SIGMOID = 0x2
 MR_ROUTER_TWO_LAUNCH = 0x4
 MR_W4_GROUP_MASK, MR_W4_ZEROS, MR_W4_SCALE_F16 = 0xFF, 0x100, 0x200
+MR_MOE_SOFTMAX = 0x1
 MR_DEVERR_GEMV_TIMEOUT, MR_DEVERR_GEMM_TIMEOUT, MR_DEVERR_TOPK_TIMEOUT, MR_DEVERR_SELFTEST = 1, 2, 4, 8
 
 EXPORTS = (
@@ -29,6 +30,7 @@ EXPORTS = (
     "gemm_f16_grouped_select_tile", "cast_f32_bf16", "gemm_f16_ex", "gemm_f16", "gemm_f16_num_tiles",
     "gemm_f16_tile_name", "gemm_f16_select_tile", "mr_poll_errors", "mr_selftest_wait_timeout",
     "mr_status_str", "mr_version", "w4_packed_bytes", "w4_pack", "mrgemv_w4",
+    "moe_window_workspace_bytes", "moe_window_bf16", "moe_window_w4",
 )
 
 
@@ -81,7 +83,14 @@ def _load() -> ctypes.CDLL:
     L.w4_packed_bytes.restype = ctypes.c_size_t
     L.w4_pack.argtypes = [P, P, P, P, ctypes.c_size_t, I32, I32, I32, U32, I32, P]
     L.mrgemv_w4.argtypes = [P, I64, P, ctypes.c_size_t, P, I64, I32, I32, I32, I32, U32, U32, P]
-    for name in ("w4_pack", "mrgemv_w4"):
+    SZ = ctypes.c_size_t
+    L.moe_window_workspace_bytes.argtypes = [I32, I32, I32, I32]
+    L.moe_window_workspace_bytes.restype = SZ
+    L.moe_window_bf16.argtypes = [P, I64, P, P, I64, P, I64, I64, P, I64, I64, P, I64, I32, I32, I32, I32, I32, I32,
+                                  I32, U32, P, SZ, P]
+    L.moe_window_w4.argtypes = [P, I64, P, P, I64, P, SZ, P, SZ, P, I64, I32, I32, I32, I32, I32, I32, U32, I32, U32,
+                                P, SZ, P]
+    for name in ("w4_pack", "mrgemv_w4", "moe_window_bf16", "moe_window_w4"):
         getattr(L, name).restype = ctypes.c_int
     for name in ("mrgemv_bf16", "mrgemv_bf16_ex", "mrgemv_bf16_plan", "router_topk", "router_topk_ex",
                  "router_topk_merge", "router_gemv_topk",
@@ -381,3 +390,49 @@ def mrgemv_w4(A, packed, C, fmt: int, stream=None, flags: int = 0) -> None:
     st = lib.mrgemv_w4(A.data_ptr(), lda, packed.data_ptr(), packed.numel() * packed.element_size(), C.data_ptr(),
                        ldc, m, n, k, _dtype_code(A), fmt, flags, _stream(stream))
     _check(st, "mrgemv_w4")
+
+
+def moe_window_workspace_bytes(m: int, topk: int, hidden: int, inter: int) -> int:
+    return int(lib.moe_window_workspace_bytes(m, topk, hidden, inter))
+
+
+def _window(X, ids, weights, Y):
+    m, hidden, ldx = _rows(X, "X")
+    mi, topk, ldr = _rows(ids, "ids")
+    my, hy, ldy = _rows(Y, "Y")
+    if mi != m or my != m or hy != hidden:
+        raise ValueError(f"shape mismatch X{tuple(X.shape)} ids{tuple(ids.shape)} Y{tuple(Y.shape)}")
+    if weights.shape != ids.shape or weights.stride() != ids.stride():
+        raise ValueError("weights must match ids' shape and stride")
+    return m, topk, hidden, ldx, ldr, ldy
+
+
+def moe_window_bf16(X, ids, weights, Wup, Wdown, Y, workspace, expert_base: int = 0, flags: int = 0,
+                    stream=None) -> None:
+    """Y[m,hidden] (fp32 or bf16) = the experts ids[m,topk] (int32) of X[m,hidden] (bf16), weighted by
+    weights[m,topk] (fp32; their softmax with MR_MOE_SOFTMAX).  Wup[experts,2*inter,hidden] holds the gate rows
+    before the up rows, Wdown is [experts,hidden,inter].  ``workspace``: a CUDA tensor of at least
+    moe_window_workspace_bytes(...) bytes."""
+    m, topk, hidden, ldx, ldr, ldy = _window(X, ids, weights, Y)
+    su, sd = Wup.stride(), Wdown.stride()
+    if len(su) != 3 or len(sd) != 3 or su[2] != 1 or sd[2] != 1:
+        raise ValueError("Wup and Wdown must be 3-D tensors with unit column stride")
+    experts, _, inter = Wdown.shape
+    if tuple(Wup.shape) != (experts, 2 * inter, hidden) or Wdown.shape[1] != hidden:
+        raise ValueError(f"shape mismatch Wup{tuple(Wup.shape)} Wdown{tuple(Wdown.shape)}")
+    st = lib.moe_window_bf16(X.data_ptr(), ldx, ids.data_ptr(), weights.data_ptr(), ldr, Wup.data_ptr(), su[1], su[0],
+                             Wdown.data_ptr(), sd[1], sd[0], Y.data_ptr(), ldy, m, topk, experts, hidden, inter,
+                             expert_base, _dtype_code(Y), flags, workspace.data_ptr(),
+                             workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "moe_window_bf16")
+
+
+def moe_window_w4(X, ids, weights, up, down, Y, workspace, experts: int, inter: int, fmt: int, expert_base: int = 0,
+                  flags: int = 0, stream=None) -> None:
+    """moe_window_bf16 with the experts' weights packed by w4_pack (``up`` paired, ``down`` not)."""
+    m, topk, hidden, ldx, ldr, ldy = _window(X, ids, weights, Y)
+    st = lib.moe_window_w4(X.data_ptr(), ldx, ids.data_ptr(), weights.data_ptr(), ldr, up.data_ptr(),
+                           up.numel() * up.element_size(), down.data_ptr(), down.numel() * down.element_size(),
+                           Y.data_ptr(), ldy, m, topk, experts, hidden, inter, expert_base, fmt, _dtype_code(Y), flags,
+                           workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "moe_window_w4")

@@ -6,3 +6,4 @@
 #include "gemm_f16.cu"
 #include "cast_bf16.cu"
 #include "mrgemv_w4.cu"
+#include "moe_window.cu"

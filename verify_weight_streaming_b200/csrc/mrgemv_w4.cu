@@ -15,8 +15,6 @@
 // neighbours, so row i of the output has the same bits for every m.
 #include "w4_core.cuh"
 
-#include <atomic>
-
 namespace mr {
 namespace w4 {
 
@@ -188,20 +186,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const Params p) {
         }
         buf ^= 1;
     }
-}
-
-// Allow `kernel` all the shared memory the device offers, once per device.
-template <class K>
-bool allow_smem(K kernel, std::atomic<uint64_t> &done) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-    const uint64_t bit = 1ull << dev;
-    if (done.load(std::memory_order_acquire) & bit) return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, mr_host::max_smem_optin()) !=
-        cudaSuccess)
-        return false;
-    done.fetch_or(bit, std::memory_order_release);
-    return true;
 }
 
 template <int G, bool F16, int NT>

@@ -13,6 +13,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace mr {
@@ -173,6 +175,63 @@ __device__ __forceinline__ void consume_block(uint32_t stage, uint32_t fmt, cons
             C[c][3] = fmaf(s8, acc[c][3], C[c][3]);
         }
     }
+}
+
+// ---- the same for a bf16 weight in row-major order ------------------------
+
+constexpr int kBlockBf16 = kTileRows * kBlockK * 2;
+
+// Request 16 rows x 128 k: `row0` and `row8` are this lane's rows g and g + 8
+// at the block's first k (on0 / on8: whether they exist), `live` the k values
+// left in the row.  Every lane copies exactly the bytes that it reads back.
+__device__ __forceinline__ void issue_block_bf16(uint32_t stage, const uint16_t *row0, const uint16_t *row8, bool on0,
+                                                 bool on8, int live, int lane) {
+    const int t = lane & 3;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int p = 32 * j + 8 * t;
+        const bool in = p < live;
+        cp_async16_zfill(stage + (2 * j) * 512 + 16 * lane, in && on0 ? row0 + p : row0, in && on0);
+        cp_async16_zfill(stage + (2 * j + 1) * 512 + 16 * lane, in && on8 ? row8 + p : row0, in && on8);
+    }
+}
+
+// C += (the block) . (the activation columns); the tensor core's own sums end
+// with the block, as in consume_block.
+template <int NT>
+__device__ __forceinline__ void consume_block_bf16(uint32_t stage, const uint32_t (&x)[NT], const bool (&on)[NT],
+                                                   float (&C)[NT][4], int lane) {
+    float acc[NT][4] = {};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint4 v0 = lds128(stage + (2 * j) * 512 + 16 * lane);
+        const uint4 v8 = lds128(stage + (2 * j + 1) * 512 + 16 * lane);
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+            uint4 b = make_uint4(0, 0, 0, 0);
+            if (on[c]) b = lds128(x[c] + 64 * j);
+            mma<false>(acc[c], v0.x, v8.x, v0.y, v8.y, b.x, b.y);
+            mma<false>(acc[c], v0.z, v8.z, v0.w, v8.w, b.z, b.w);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) C[c][i] += acc[c][i];
+}
+
+// Allow `kernel` all the shared memory the device offers, once per device.
+template <class K>
+bool allow_smem(K kernel, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    const uint64_t bit = 1ull << dev;
+    if (done.load(std::memory_order_acquire) & bit) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, mr_host::max_smem_optin()) !=
+        cudaSuccess)
+        return false;
+    done.fetch_or(bit, std::memory_order_release);
+    return true;
 }
 
 }  // namespace w4
