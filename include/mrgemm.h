@@ -251,6 +251,38 @@ mr_status router_topk_merge(const float *cand_val, const int32_t *cand_idx, int3
                             int64_t ldo, void *stream);
 
 /*
+ * token_logprobs -- what a sampler or a scorer asks of a row of logits, in one
+ * pass over them.  With z = scale * logits[r] (scale: an inverse temperature),
+ *
+ *   lse[r]               = log sum_j exp(z_j)
+ *   logprob[r][i]        = z_v - lse[r] for v = tokens[r][i]
+ *   entropy[r]           = -sum_j p_j log p_j,  p = softmax(z)
+ *   top_idx[r][t]        = router_topk's choice of rank t (ties to the lower index)
+ *   top_logprob[r][t]    = its log probability
+ *
+ * logits : m rows of n values of dtype (MR_F32, MR_BF16 or MR_F16), row stride
+ *          ldl (>= n); any row may start anywhere (natural alignment).
+ * tokens, logprob : m rows of ntok int32 / fp32, row strides ldt, ldp; NULL
+ *          with ntok 0.  A token outside [0, n) (padding) gets NaN.
+ * lse, entropy : m fp32, or NULL.
+ * top_idx, top_logprob : m rows of topk int32 / fp32, row stride ldo; NULL with
+ *          topk 0 (top_logprob may be NULL alone).
+ * 0 <= topk <= min(n, 32), 0 <= ntok <= 256, n <= 2^30, 1e-6 <= scale <= 1e6; some
+ * output is asked for.
+ * A logit of -inf has probability 0 and adds nothing to the entropy.  Where it
+ * is undefined a result is NaN: every one of a row with a NaN; log
+ * probabilities and entropy of a row of nothing but -inf (lse -inf); the
+ * entropy of a row with +inf, and its +inf logits' log probabilities (lse +inf,
+ * the others -inf).  top_idx is defined for all of these.
+ * Sums are fp32.  A row's bits depend on its values, n, dtype, scale and the
+ * row's address modulo 16, not on m or the other rows.
+ */
+mr_status token_logprobs(const void *logits, int64_t ldl, int32_t dtype, int32_t m, int32_t n, float scale,
+                         const int32_t *tokens, int64_t ldt, int32_t ntok, float *logprob, int64_t ldp,
+                         float *lse, float *entropy, int32_t topk, int32_t *top_idx, float *top_logprob,
+                         int64_t ldo, void *stream);
+
+/*
  * cast_f32_bf16 -- fp32 -> bf16, round to nearest even, for `rows` rows of
  * `cols` values in one launch: the bf16 cast of the verify window's rows in
  * Strata PR #109 ("What": one call, the rows are contiguous), which feeds the

@@ -31,6 +31,7 @@ EXPORTS = (
     "gemm_f16_tile_name", "gemm_f16_select_tile", "mr_poll_errors", "mr_selftest_wait_timeout",
     "mr_status_str", "mr_version", "w4_packed_bytes", "w4_pack", "mrgemv_w4",
     "moe_window_workspace_bytes", "moe_window_bf16", "moe_window_w4",
+    "token_logprobs",
 )
 
 
@@ -90,7 +91,8 @@ def _load() -> ctypes.CDLL:
                                   I32, U32, P, SZ, P]
     L.moe_window_w4.argtypes = [P, I64, P, P, I64, P, SZ, P, SZ, P, I64, I32, I32, I32, I32, I32, I32, U32, I32, U32,
                                 P, SZ, P]
-    for name in ("w4_pack", "mrgemv_w4", "moe_window_bf16", "moe_window_w4"):
+    L.token_logprobs.argtypes = [P, I64, I32, I32, I32, ctypes.c_float, P, I64, I32, P, I64, P, P, I32, P, P, I64, P]
+    for name in ("w4_pack", "mrgemv_w4", "moe_window_bf16", "moe_window_w4", "token_logprobs"):
         getattr(L, name).restype = ctypes.c_int
     for name in ("mrgemv_bf16", "mrgemv_bf16_ex", "mrgemv_bf16_plan", "router_topk", "router_topk_ex",
                  "router_topk_merge", "router_gemv_topk",
@@ -436,3 +438,42 @@ def moe_window_w4(X, ids, weights, up, down, Y, workspace, experts: int, inter: 
                            Y.data_ptr(), ldy, m, topk, experts, hidden, inter, expert_base, fmt, _dtype_code(Y), flags,
                            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st, "moe_window_w4")
+
+
+def token_logprobs(logits, tokens=None, logprob=None, scale: float = 1.0, lse=None, entropy=None, top_idx=None,
+                   top_logprob=None, stream=None) -> None:
+    """Log probabilities (fp32) of logits[m,n] (fp32, bf16 or f16) times ``scale``, into whichever outputs are given:
+    logprob[m,t] of tokens[m,t] (int32), lse[m], entropy[m], and the top_idx.shape[1] best alternatives
+    top_idx[m,k] (int32), top_logprob[m,k]."""
+    import torch
+    m, n, ldl = _rows(logits, "logits")
+    dtype = -1 if logits.dtype == torch.int16 else _dtype_code(logits)
+    tptr = lptr = iptr = vptr = None
+    ntok = ldt = ldp = topk = ldo = 0
+    if (tokens is None) != (logprob is None):
+        raise ValueError("tokens and logprob go together")
+    if tokens is not None:
+        if tokens.dim() != 2 or tokens.shape[0] != m or logprob.shape != tokens.shape:
+            raise ValueError("tokens and logprob must be [m, t]")
+        if tokens.shape[1]:
+            _, ntok, ldt = _rows(tokens, "tokens")
+            ldp = _rows(logprob, "logprob")[2]
+            tptr, lptr = tokens.data_ptr(), logprob.data_ptr()
+    for t, name in ((lse, "lse"), (entropy, "entropy")):
+        if t is not None and (t.dim() != 1 or t.shape[0] != m or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous [m] tensor")
+    if top_idx is None and top_logprob is not None:
+        raise ValueError("top_logprob needs top_idx")
+    if top_idx is not None:
+        if top_idx.dim() != 2 or top_idx.shape[0] != m:
+            raise ValueError("top_idx must be [m, k]")
+        if top_logprob is not None and (top_logprob.shape != top_idx.shape or top_logprob.stride() != top_idx.stride()):
+            raise ValueError("top_logprob must match top_idx's shape and stride")
+        if top_idx.shape[1]:
+            _, topk, ldo = _rows(top_idx, "top_idx")
+            iptr = top_idx.data_ptr()
+            vptr = None if top_logprob is None else top_logprob.data_ptr()
+    st = lib.token_logprobs(logits.data_ptr(), ldl, dtype, m, n, scale, tptr, ldt, ntok, lptr, ldp,
+                            None if lse is None else lse.data_ptr(), None if entropy is None else entropy.data_ptr(),
+                            topk, iptr, vptr, ldo, _stream(stream))
+    _check(st, "token_logprobs")

@@ -7,3 +7,4 @@
 #include "cast_bf16.cu"
 #include "mrgemv_w4.cu"
 #include "moe_window.cu"
+#include "token_logprobs.cu"
