@@ -309,8 +309,9 @@ mr_status cast_f32_bf16(const float *X, int64_t ldx, void *Y, int64_t ldy, int32
  *
  * The packed order: tiles of 16 weight rows; a tile's k in blocks of 128, one
  * after the other (the last one padded with zero weight, and rows past n
- * too); a block is 1024 bytes of values, then the scales [128 / G][16 rows],
- * then the zero points [128 / G][16 rows], one byte each.  Value bytes: for
+ * too); a block is 1024 bytes of values, then the scales [8][2][128 / G] of
+ * rows g and 8 + g for g = 0..7, then the zero points in the same order, one
+ * byte each.  Value bytes: for
  * half h = 0, 1 and l = 4g + t = 0..31, four 32-bit words of row 8h + g, word
  * j holding k = 32j + 8t .. + 7: nibble i is value 2i, nibble 4 + i is value
  * 2i + 1.  With `paired` the rows are two halves of equal length (a gate and

@@ -8,18 +8,26 @@
 // launch) and the flat list of (expert, tile) is cut into equal runs.
 //
 //  * up kernel: a tile is 8 gate rows and the 8 up rows of the same columns,
-//    one 16-row operand of the matrix instruction; a warp takes a tile and a
-//    quarter of k and stores its partial sums.
-//  * down kernel: adds the quarters in order, applies the activation, and
-//    multiplies by the down projection.  h is fp32; the tensor core takes it
-//    as three bf16 pieces whose sum is exact, as three columns of the 8 that
-//    an instruction has (most experts serve one or two rows), so no
-//    precision is lost between the two products and no instruction added.
+//    one 16-row operand of the matrix instruction.  k is summed in quarters,
+//    one warp each while tiles are few, all four in one warp when there are
+//    enough tiles to keep the warps busy; either way the quarters are added
+//    in order.
+//  * down kernel: applies the activation and multiplies by the down
+//    projection.  h is fp32; the tensor core takes it as three bf16 pieces
+//    whose sum is exact, as three columns of the 8 that an instruction has (most
+//    experts serve one or two rows), so no precision is lost between the two
+//    products and no instruction added.
 //  * combine kernel: the weighted sum over a row's choices, in their order.
+//    (Added up instead by the warp that stores a tile's last share, it took
+//    323 us in place of 234 at 16 rows: a few warps get most of that work.)
 //
+// The three overlap by programmatic launch: down requests its first weights
+// and combine computes its softmax before the kernel ahead has finished.
 // The split of k depends on the sizes of the expert alone and sums run in a
 // fixed order, so a row's bits depend on its own x, ids and weights only.
 #include "w4_core.cuh"
+
+#include <type_traits>
 
 namespace mr {
 namespace moe {
@@ -31,8 +39,6 @@ constexpr int kMaxTopk = 32;
 constexpr int kMaxSlots = kMaxRows * kMaxTopk;
 constexpr int kChunk = 8;        // choices of one expert that share a pass over its weight
 constexpr int kSplit = 4;        // parts of k in the up projection
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 
 struct Params {
     const uint8_t *X;
@@ -42,20 +48,21 @@ struct Params {
     int64_t ldr;
     const uint8_t *Wu, *Wd;
     int64_t ldu, ldd, eu, ed;     // bytes: row strides (bf16) and expert strides
-    float *part;                  // [slot][kSplit][2 * inter]
+    float *part;                  // [slot][1 or kSplit][2 * inter]
     float *down;                  // [slot][hidden]
     void *Y;
     int64_t ldy;
     int m, topk, experts, base, hidden, inter;
     int cap;                      // choices per chunk: min(kChunk, m)
-    int block;                    // bytes of a ring stage
-    int stages;
+    int block;                    // bytes of a block of weight
+    int per_up, slots_up, per_down, slots_down;  // ring stages, as in mrgemv_w4
+    int up_warps;                 // warps of the up kernel's grid
     int out_bf16, softmax;
     uint32_t fmt;
 };
 
 // The chunks of a call: up to `cap` choices (slots t * topk + s) of one expert.
-struct Chunks {
+struct alignas(16) Chunks {
     int32_t ids[kMaxSlots];
     uint32_t lead[kMaxSlots / 32];
     int32_t expert[kMaxSlots];
@@ -67,9 +74,14 @@ constexpr int kChunkBytes = (sizeof(Chunks) + 127) / 128 * 128;  // at the start
 
 // Built by every thread of the CTA; deterministic (chunks in the order of
 // their first slot).
+template <int kThreads>
 __device__ void build_chunks(Chunks &c, const Params &p) {
     const int S = p.m * p.topk, lane = threadIdx.x & 31;
-    for (int s = threadIdx.x; s < S; s += kThreads) {
+    for (int s = threadIdx.x; s < kMaxSlots; s += kThreads) {
+        if (s >= S) {
+            c.ids[s] = -1;
+            continue;
+        }
         // from L2: the producer of ids may have run while this grid was starting
         const int64_t e = (int64_t)__ldcg(p.ids + (s / p.topk) * p.ldr + s % p.topk);
         c.ids[s] = (e >= p.base && e - p.base < p.experts) ? (int32_t)(e - p.base) : -1;
@@ -83,12 +95,19 @@ __device__ void build_chunks(Chunks &c, const Params &p) {
         const int e = s < S ? c.ids[s] : -1;
         int n = 0, first = s;
         if (e >= 0) {
-            for (int q = 0; q < s; ++q)
-                if (c.ids[q] == e) {
-                    if (n % p.cap == 0) first = q;
-                    ++n;
-                }
-            if (n % p.cap == 0) first = s;
+            int of = 0;  // n % cap
+            for (int q = 0; q < s; q += 4) {
+                const int4 v = *reinterpret_cast<const int4 *>(c.ids + q);
+                const int four[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (four[j] == e && q + j < s) {
+                        if (of == 0) first = q + j;
+                        of = of + 1 == p.cap ? 0 : of + 1;
+                        ++n;
+                    }
+            }
+            if (of == 0) first = s;
         }
         rank[i] = n;
         lead[i] = first;
@@ -117,202 +136,177 @@ __device__ void build_chunks(Chunks &c, const Params &p) {
 
 __host__ __device__ inline int row_stride(int k) { return (k + kBlockK - 1) / kBlockK * kBlockK * 2 + 64; }
 
+// The stream of a warp's weight blocks: packed 4-bit blocks come through a Ring
+// (bulk copies of up to `per` blocks), bf16 rows through cp.async, where every
+// lane copies the bytes it reads itself.
+
+// Whether a warp of the up kernel sums all quarters of a tile itself: when
+// that still gives every warp four tiles (8 rows of 4-bit experts, 6000 tiles,
+// 2368 warps: quarters; 16 rows: whole tiles).
+__device__ __forceinline__ bool whole_tiles(const Params &p, int chunks) {
+    return chunks * (p.inter / 8) >= 4 * p.up_warps;
+}
+
 // ---- up projection --------------------------------------------------------
 
-// G = 0: bf16 rows; else 4-bit groups of G.
-template <int G>
-__global__ void __launch_bounds__(kThreads) up_kernel(const Params p) {
+// G = 0: bf16 rows, STAGES blocks in flight; else 4-bit groups of G.
+template <int G, int WARPS, int STAGES>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) up_kernel(const Params p) {
     extern __shared__ __align__(128) uint8_t smem_base[];
     Chunks &chunks = *reinterpret_cast<Chunks *>(smem_base);
     uint8_t *smem = smem_base + kChunkBytes;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int kblocks = (p.hidden + kBlockK - 1) / kBlockK, tiles = p.inter / 8, xs = row_stride(p.hidden);
-    const uint32_t x0 = smem_u32(smem), ring = x0 + p.m * xs + warp * p.stages * p.block;
+    const uint32_t x0 = smem_u32(smem), ring0 = x0 + (p.m + 1) * xs;
+    const int ring_bytes = p.slots_up * p.per_up * p.block;
+    Ring ring(ring0 + warp * ring_bytes, ring0 + WARPS * ring_bytes + warp * p.slots_up * 8, p.slots_up,
+              p.per_up * p.block);
+    if (G) ring.init(lane);
     grid_dependency_wait();
     grid_launch_dependents();  // after the wait: the next grid may read ids at once
-    build_chunks(chunks, p);
-
-    const int64_t items = (int64_t)chunks.n * tiles * kSplit;
-    const int64_t i0 = items * blockIdx.x / gridDim.x, i1 = items * (blockIdx.x + 1) / gridDim.x;
-    auto from = [&](int64_t i) { return kblocks * (int)(i % kSplit) / kSplit; };
-    auto to = [&](int64_t i) { return kblocks * ((int)(i % kSplit) + 1) / kSplit; };
-    // the next block to request
-    int64_t ri = i0 + warp;
-    int rkb = 0, rend = 0;
-    const uint8_t *src0 = nullptr, *src8 = nullptr;
-    auto aim = [&]() {  // first item from ri on that has blocks
-        for (; ri < i1; ri += kWarps) {
-            rkb = from(ri);
-            rend = to(ri);
-            if (rkb < rend) break;
+    // The rows, and one of zeros, on their way while the chunks are built.
+    const int pieces = kblocks * (kBlockK / 8), live = p.hidden / 8;
+    for (int r = warp; r <= p.m; r += WARPS)
+        for (int c = lane; c < pieces; c += 32) {
+            const bool in = r < p.m && c < live;
+            cp_async16_zfill(x0 + r * xs + 16 * c, in ? p.X + r * p.ldx + 16 * c : p.X, in);
         }
-        if (ri >= i1) return;
-        const int unit = (int)(ri / kSplit), tile = unit % tiles;
-        const uint8_t *w = p.Wu + (int64_t)chunks.expert[unit / tiles] * p.eu;
+    cp_async_commit();
+    build_chunks<WARPS * 32>(chunks, p);
+
+    // This CTA's run of items (tiles, or quarters of them), a warp every
+    // WARPS-th: a warp of quarters always has the same one.
+    const bool whole = whole_tiles(p, chunks.n);
+    const int shift = whole ? 0 : 2, parts = whole ? 1 : kSplit;
+    const int64_t items = (int64_t)(chunks.n * tiles) << shift;
+    const int i0 = (int)(items * blockIdx.x / gridDim.x) + warp, i1 = (int)(items * (blockIdx.x + 1) / gridDim.x);
+    const int slice = whole ? 0 : i0 & 3, step = WARPS >> shift;
+    const int kb0 = kblocks * slice / kSplit, kb1 = whole ? kblocks : kblocks * (slice + 1) / kSplit;
+    int left = i0 < i1 ? (i1 - i0 + WARPS - 1) / WARPS : 0;  // items of this warp
+    int chunk = (i0 >> shift) / tiles, tile = (i0 >> shift) % tiles;
+
+    // the next blocks to request
+    int rleft = kb0 < kb1 ? left : 0, rchunk = chunk, rtile = tile, rkb = kb0;
+    const uint8_t *src0 = nullptr, *src8 = nullptr;
+    auto aim = [&]() {
+        const uint8_t *w = p.Wu + (int64_t)chunks.expert[rchunk] * p.eu;
         if (G) {
-            src0 = w + (int64_t)tile * kblocks * p.block;
+            src0 = w + (int64_t)(rtile * kblocks) * p.block;
         } else {
-            src0 = w + (int64_t)(tile * 8 + g) * p.ldu;
+            src0 = w + (int64_t)(rtile * 8 + g) * p.ldu;
             src8 = src0 + (int64_t)p.inter * p.ldu;
         }
     };
-    aim();
+    if (rleft) aim();
     auto request = [&](int stage) {
-        if (ri < i1) {
-            const uint32_t dst = ring + stage * p.block;
+        if (rleft) {
+            const int count = G ? min(p.per_up, kb1 - rkb) : 1;
             if (G)
-                issue_block(dst, src0 + (int64_t)rkb * p.block, p.block, lane);
+                ring.request(src0 + rkb * p.block, count * p.block, lane);
             else
-                issue_block_bf16(dst, reinterpret_cast<const uint16_t *>(src0) + rkb * kBlockK,
+                issue_block_bf16(ring.data + stage * p.block, reinterpret_cast<const uint16_t *>(src0) + rkb * kBlockK,
                                  reinterpret_cast<const uint16_t *>(src8) + rkb * kBlockK, true, true,
                                  p.hidden - rkb * kBlockK, lane);
-            if (++rkb == rend) {
-                ri += kWarps;
-                aim();
+            rkb += count;
+            if (rkb == kb1) {
+                rkb = kb0;
+                rtile += step;
+                while (rtile >= tiles) {
+                    rtile -= tiles;
+                    ++rchunk;
+                }
+                if (--rleft) aim();
             }
         }
-        cp_async_commit();
+        if (!G) cp_async_commit();
     };
-    constexpr int kStages = G ? 8 : 2;
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) request(s);
-
-    const int pieces = kblocks * (kBlockK / 8), live = p.hidden / 8;
-    for (int e = threadIdx.x; e < p.m * pieces; e += kThreads) {
-        const int r = e / pieces, c = e % pieces;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (c < live) v = *reinterpret_cast<const uint4 *>(p.X + r * p.ldx + 16 * c);
-        *reinterpret_cast<uint4 *>(smem + r * xs + 16 * c) = v;
-    }
+    const int slots = G ? p.slots_up : STAGES;
+    for (int s = 0; s < slots; ++s) request(s);
+    cp_async_wait<G ? 0 : STAGES>();  // the rows
     __syncthreads();
 
     int stage = 0;
-    for (int64_t i = i0 + warp; i < i1; i += kWarps) {
-        const int unit = (int)(i / kSplit), chunk = unit / tiles, tile = unit % tiles, slice = (int)(i % kSplit);
+    for (; left; --left) {
         const int count = chunks.count[chunk];
-        const bool on[1] = {g < count};
-        const uint32_t xb = x0 + (on[0] ? chunks.slot[chunk][g] / p.topk : 0) * xs + 16 * t;
-        float C[1][4] = {};
-        for (int kb = from(i); kb < to(i); ++kb) {
-            cp_async_wait<kStages - 1>();
-            __syncwarp();
-            const uint32_t x[1] = {xb + kb * (kBlockK * 2)};
-            if constexpr (G)
-                consume_block<G, false, 1>(ring + stage * p.block, p.fmt, x, on, C, lane);
-            else
-                consume_block_bf16<1>(ring + stage * p.block, x, on, C, lane);
-            __syncwarp();
-            request(stage);
-            stage = stage + 1 == kStages ? 0 : stage + 1;
+        const uint32_t xb = x0 + (g < count ? chunks.slot[chunk][g] / p.topk : p.m) * xs + 16 * t;
+        float C[1][4] = {}, sum[4] = {};
+        int next = kblocks * (slice + 1) / kSplit, quarter = slice;  // where the quarter ends
+        auto close = [&](int kb) {  // quarters that end at block kb join the sum
+            while (whole && kb == next && quarter < kSplit) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    sum[e] += C[0][e];
+                    C[0][e] = 0.0f;
+                }
+                ++quarter;
+                next = kblocks * (quarter + 1) / kSplit;
+            }
+        };
+        close(0);
+        if constexpr (G) {
+            for (int kb = kb0; kb < kb1; kb += p.per_up) {
+                const uint32_t at = ring.wait();
+                const int blocks = min(p.per_up, kb1 - kb);
+#pragma unroll 1
+                for (int b = 0; b < blocks; ++b) {
+                    const uint32_t x[1] = {xb + (kb + b) * (kBlockK * 2)};
+                    consume_block<G, false, 1>(at + b * p.block, p.fmt, x, C, lane);
+                    close(kb + b + 1);
+                }
+                ring.done();
+                request(0);
+            }
+        } else {
+            for (int kb = kb0; kb < kb1; ++kb) {
+                cp_async_wait<STAGES - 1>();
+                const uint32_t x[1] = {xb + kb * (kBlockK * 2)};
+                consume_block_bf16<1>(ring.data + stage * p.block, x, C, lane);
+                close(kb + 1);
+                request(stage);
+                stage = stage + 1 == STAGES ? 0 : stage + 1;
+            }
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             if (2 * t + h < count) {
-                float *out = p.part + ((int64_t)chunks.slot[chunk][2 * t + h] * kSplit + slice) * 2 * p.inter +
+                float *out = p.part + (int64_t)(chunks.slot[chunk][2 * t + h] * parts + slice) * 2 * p.inter +
                              tile * 8 + g;
-                out[0] = C[0][h];
-                out[p.inter] = C[0][2 + h];
+                out[0] = whole ? sum[h] : C[0][h];
+                out[p.inter] = whole ? sum[2 + h] : C[0][2 + h];
             }
+        tile += step;
+        while (tile >= tiles) {
+            tile -= tiles;
+            ++chunk;
+        }
     }
 }
 
-// ---- activation and down projection ---------------------------------------
+// ---- activation and down projection ----------------------------------------
 
-template <int G, int NT>
-__device__ __forceinline__ void down_block(uint32_t stage, uint32_t fmt, uint32_t h0, int hs, int kb, int count,
-                                           float (&C)[4][4], int lane) {
-    const int g = lane >> 2, t = lane & 3;
-    bool on[NT];
-    uint32_t x[NT];
-    float D[NT][4];
-#pragma unroll
-    for (int c = 0; c < NT; ++c) {
-        const int i = 2 * c + (g >> 2), piece = g & 3;  // column g: piece of choice i
-        on[c] = piece < 3 && i < count;
-        x[c] = h0 + (on[c] ? i * 3 + piece : 0) * hs + kb * (kBlockK * 2) + 16 * t;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) D[c][e] = C[c][e];
-    }
-    if constexpr (G)
-        consume_block<G, false, NT>(stage, fmt, x, on, D, lane);
-    else
-        consume_block_bf16<NT>(stage, x, on, D, lane);
-#pragma unroll
-    for (int c = 0; c < NT; ++c)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) C[c][e] = D[c][e];
-}
-
-template <int G>
-__global__ void __launch_bounds__(kThreads) down_kernel(const Params p) {
-    extern __shared__ __align__(128) uint8_t smem_base[];
-    Chunks &chunks = *reinterpret_cast<Chunks *>(smem_base);
-    uint8_t *smem = smem_base + kChunkBytes;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int kblocks = (p.inter + kBlockK - 1) / kBlockK, tiles = (p.hidden + kTileRows - 1) / kTileRows;
-    const int hs = row_stride(p.inter);
-    const uint32_t h0 = smem_u32(smem), ring = h0 + 3 * p.cap * hs + warp * p.stages * p.block;
-    grid_launch_dependents();
-    build_chunks(chunks, p);
-
-    const int64_t units = (int64_t)chunks.n * tiles;
-    const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
-    int64_t ru = u0 + warp;
-    int rkb = 0;
-    const uint8_t *src0 = nullptr, *src8 = nullptr;
-    bool on0 = false, on8 = false;
-    auto aim = [&]() {
-        if (ru >= u1) return;
-        const int tile = (int)(ru % tiles);
-        const uint8_t *w = p.Wd + (int64_t)chunks.expert[ru / tiles] * p.ed;
-        if (G) {
-            src0 = w + (int64_t)tile * kblocks * p.block;
-        } else {
-            const int row = tile * kTileRows + g;
-            on0 = row < p.hidden;
-            on8 = row + 8 < p.hidden;
-            src0 = on0 ? w + (int64_t)row * p.ldd : w;
-            src8 = on8 ? w + (int64_t)(row + 8) * p.ldd : w;
-        }
-    };
-    aim();
-    auto request = [&](int stage) {
-        if (ru < u1) {
-            const uint32_t dst = ring + stage * p.block;
-            if (G)
-                issue_block(dst, src0 + (int64_t)rkb * p.block, p.block, lane);
-            else
-                issue_block_bf16(dst, reinterpret_cast<const uint16_t *>(src0) + rkb * kBlockK,
-                                 reinterpret_cast<const uint16_t *>(src8) + rkb * kBlockK, on0, on8,
-                                 p.inter - rkb * kBlockK, lane);
-            if (++rkb == kblocks) {
-                rkb = 0;
-                ru += kWarps;
-                aim();
-            }
-        }
-        cp_async_commit();
-    };
-    constexpr int kStages = G ? 8 : 2;
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) request(s);
-
-    grid_dependency_wait();  // the up projection's partial sums
-    int stage = 0;
-    int64_t u = u0 + warp;
-    for (int chunk = (int)(u0 / tiles); u0 < u1 && chunk <= (int)((u1 - 1) / tiles); ++chunk) {
-        const int count = chunks.count[chunk], width = kblocks * kBlockK;
-        __syncthreads();  // the chunk before is done with h
-        for (int e = threadIdx.x; e < count * width; e += kThreads) {
-            const int i = e / width, j = e % width;
+// A chunk's activations in fp32 as three bf16 rows each, hi + mid + lo.
+template <int THREADS>
+__device__ void stage_activations(uint8_t *smem, const Params &p, const Chunks &c, int chunk, int parts, int hs,
+                                  int width) {
+    for (int i = 0; i < c.count[chunk]; ++i) {
+        const float *q0 = p.part + (int64_t)c.slot[chunk][i] * parts * 2 * p.inter;
+        for (int j = threadIdx.x; j < width; j += THREADS) {
             float h = 0.0f;
             if (j < p.inter) {
-                const float *q = p.part + (int64_t)chunks.slot[chunk][i] * kSplit * 2 * p.inter + j;
-                float gate = 0.0f, up = 0.0f;
+                const float *q = q0 + j;
+                float gate = q[0], up = q[p.inter];
+                if (parts > 1) {
+                    float v[2 * (kSplit - 1)];
 #pragma unroll
-                for (int s = 0; s < kSplit; ++s) {
-                    gate += q[(int64_t)s * 2 * p.inter];
-                    up += q[(int64_t)s * 2 * p.inter + p.inter];
+                    for (int s = 0; s < kSplit - 1; ++s) {
+                        v[2 * s] = q[(2 * s + 2) * p.inter];
+                        v[2 * s + 1] = q[(2 * s + 3) * p.inter];
+                    }
+#pragma unroll
+                    for (int s = 0; s < kSplit - 1; ++s) {
+                        gate += v[2 * s];
+                        up += v[2 * s + 1];
+                    }
                 }
                 h = gate / (1.0f + expf(-gate)) * up;
             }
@@ -327,36 +321,150 @@ __global__ void __launch_bounds__(kThreads) down_kernel(const Params p) {
             *reinterpret_cast<uint16_t *>(row + hs) = (uint16_t)(mid >> 16);
             *reinterpret_cast<uint16_t *>(row + 2 * hs) = (uint16_t)(lo >> 16);
         }
-        __syncthreads();
-        const int64_t end = min(u1, (int64_t)(chunk + 1) * tiles);
-        for (; u < end; u += kWarps) {
-            const int tile = (int)(u - (int64_t)chunk * tiles);
-            float C[4][4] = {};
-            for (int kb = 0; kb < kblocks; ++kb) {
-                cp_async_wait<kStages - 1>();
-                __syncwarp();
-                const uint32_t at = ring + stage * p.block;
-                if (count <= 2)
-                    down_block<G, 1>(at, p.fmt, h0, hs, kb, count, C, lane);
-                else if (count <= 4)
-                    down_block<G, 2>(at, p.fmt, h0, hs, kb, count, C, lane);
-                else
-                    down_block<G, 4>(at, p.fmt, h0, hs, kb, count, C, lane);
-                __syncwarp();
-                request(stage);
-                stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+}
+
+template <int G, int WARPS, int STAGES>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) down_kernel(const Params p) {
+    extern __shared__ __align__(128) uint8_t smem_base[];
+    Chunks &chunks = *reinterpret_cast<Chunks *>(smem_base);
+    uint8_t *smem = smem_base + kChunkBytes;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int kblocks = (p.inter + kBlockK - 1) / kBlockK, tiles = (p.hidden + kTileRows - 1) / kTileRows;
+    const int hs = row_stride(p.inter), zero_row = 3 * p.cap;
+    const uint32_t h0 = smem_u32(smem), ring0 = h0 + (zero_row + 1) * hs;
+    const int ring_bytes = p.slots_down * p.per_down * p.block;
+    Ring ring(ring0 + warp * ring_bytes, ring0 + WARPS * ring_bytes + warp * p.slots_down * 8, p.slots_down,
+              p.per_down * p.block);
+    grid_launch_dependents();
+    if (G) ring.init(lane);
+    build_chunks<WARPS * 32>(chunks, p);
+
+    const int64_t units = (int64_t)chunks.n * tiles;
+    const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
+    int ru = u0 + warp, rkb = 0, rchunk = ru / tiles, rtile = ru % tiles;
+    const uint8_t *src0 = nullptr, *src8 = nullptr;
+    bool on0 = false, on8 = false;
+    auto aim = [&]() {
+        const uint8_t *w = p.Wd + (int64_t)chunks.expert[rchunk] * p.ed;
+        if (G) {
+            src0 = w + (int64_t)(rtile * kblocks) * p.block;
+        } else {
+            const int row = rtile * kTileRows + g;
+            on0 = row < p.hidden;
+            on8 = row + 8 < p.hidden;
+            src0 = on0 ? w + (int64_t)row * p.ldd : w;
+            src8 = on8 ? w + (int64_t)(row + 8) * p.ldd : w;
+        }
+    };
+    if (ru < u1) aim();
+    auto request = [&](int stage) {
+        if (ru < u1) {
+            const int count = G ? min(p.per_down, kblocks - rkb) : 1;
+            if (G)
+                ring.request(src0 + rkb * p.block, count * p.block, lane);
+            else
+                issue_block_bf16(ring.data + stage * p.block, reinterpret_cast<const uint16_t *>(src0) + rkb * kBlockK,
+                                 reinterpret_cast<const uint16_t *>(src8) + rkb * kBlockK, on0, on8,
+                                 p.inter - rkb * kBlockK, lane);
+            rkb += count;
+            if (rkb == kblocks) {
+                rkb = 0;
+                ru += WARPS;
+                rtile += WARPS;
+                while (rtile >= tiles) {
+                    rtile -= tiles;
+                    ++rchunk;
+                }
+                if (ru < u1) aim();
             }
-            // The pieces of a choice lie in lanes t = 0, 1 or t = 2, 3.
+        }
+        if (!G) cp_async_commit();
+    };
+    const int slots = G ? p.slots_down : STAGES;
+    for (int s = 0; s < slots; ++s) request(s);
+    for (int e = threadIdx.x; e < hs / 16; e += WARPS * 32)
+        *reinterpret_cast<uint4 *>(smem + zero_row * hs + 16 * e) = make_uint4(0, 0, 0, 0);
+
+    grid_dependency_wait();  // the up projection's partial sums
+    if (u0 >= u1) return;
+    const int parts = whole_tiles(p, chunks.n) ? 1 : kSplit;
+    int stage = 0;
+    // The address of a lane's column of column tile c: piece g % 4 of choice
+    // 2c + g / 4, zeros for the fourth and for choices that are not there.
+    auto column = [&](int c, int count) {
+        const int i = 2 * c + (g >> 2), piece = g & 3;
+        return h0 + (piece < 3 && i < count ? i * 3 + piece : zero_row) * hs + 16 * t;
+    };
+    // One tile of the chunk whose activations are staged.  NT column tiles of
+    // two choices a pass, and PASSES passes over a stage.
+    auto product = [&](auto nt, auto ps, int chunk, int tile, int count) {
+        constexpr int NT = decltype(nt)::value, PASSES = decltype(ps)::value;
+        uint32_t xb[PASSES][NT];
+        float C[PASSES][NT][4] = {};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (2 * c >= count) break;
-                float r0 = C[c][0] + C[c][1], r8 = C[c][2] + C[c][3];
+        for (int q = 0; q < PASSES; ++q)
+#pragma unroll
+            for (int c = 0; c < NT; ++c) xb[q][c] = column(q * NT + c, count);
+        auto one = [&](uint32_t at, int kb) {
+#pragma unroll
+            for (int q = 0; q < PASSES; ++q) {
+                uint32_t x[NT];
+#pragma unroll
+                for (int c = 0; c < NT; ++c) x[c] = xb[q][c] + kb * (kBlockK * 2);
+                if constexpr (G)
+                    consume_block<G, false, NT>(at, p.fmt, x, C[q], lane);
+                else
+                    consume_block_bf16<NT>(at, x, C[q], lane);
+            }
+        };
+        if constexpr (G) {
+            for (int kb = 0; kb < kblocks; kb += p.per_down) {
+                const uint32_t at = ring.wait();
+                const int blocks = min(p.per_down, kblocks - kb);
+#pragma unroll 1
+                for (int b = 0; b < blocks; ++b) one(at + b * p.block, kb + b);
+                ring.done();
+                request(0);
+            }
+        } else {
+            for (int kb = 0; kb < kblocks; ++kb) {
+                cp_async_wait<STAGES - 1>();
+                one(ring.data + stage * p.block, kb);
+                request(stage);
+                stage = stage + 1 == STAGES ? 0 : stage + 1;
+            }
+        }
+        // The pieces of a choice lie in lanes t = 0, 1 or t = 2, 3.
+#pragma unroll
+        for (int q = 0; q < PASSES; ++q)
+#pragma unroll
+            for (int c = 0; c < NT; ++c) {
+                float r0 = C[q][c][0] + C[q][c][1], r8 = C[q][c][2] + C[q][c][3];
                 r0 += __shfl_xor_sync(0xffffffffu, r0, 1);
                 r8 += __shfl_xor_sync(0xffffffffu, r8, 1);
-                const int i = 2 * c + (t >> 1), row = tile * kTileRows + g + 8 * (t & 1);
+                const int i = 2 * (q * NT + c) + (t >> 1), row = tile * kTileRows + g + 8 * (t & 1);
                 if (i < count && row < p.hidden)
                     p.down[(int64_t)chunks.slot[chunk][i] * p.hidden + row] = (t & 1) ? r8 : r0;
             }
+    };
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
+    int u = u0 + warp;
+    for (int chunk = u0 / tiles; chunk <= (u1 - 1) / tiles; ++chunk) {
+        const int count = chunks.count[chunk];
+        __syncthreads();  // the chunk before is done with the activations
+        stage_activations<WARPS * 32>(smem, p, chunks, chunk, parts, hs, kblocks * kBlockK);
+        __syncthreads();
+        const int end = min(u1, (chunk + 1) * tiles);
+        for (; u < end; u += WARPS) {
+            const int tile = u - chunk * tiles;
+            if (count <= 2)
+                product(One{}, One{}, chunk, tile, count);
+            else if (count <= 4)
+                product(Two{}, One{}, chunk, tile, count);
+            else
+                product(Two{}, Two{}, chunk, tile, count);
         }
     }
 }
@@ -365,13 +473,13 @@ __global__ void __launch_bounds__(kThreads) down_kernel(const Params p) {
 
 __global__ void __launch_bounds__(128) combine_kernel(const Params p) {
     __shared__ float w[kMaxTopk];
+    __shared__ int held[kMaxTopk];
     const int row = blockIdx.y;
     grid_launch_dependents();
-    grid_dependency_wait();
     if (threadIdx.x < 32) {
         const int s = threadIdx.x;
-        const int64_t e = s < p.topk ? (int64_t)p.ids[row * p.ldr + s] : -1;
-        float v = s < p.topk && e >= 0 ? p.wts[row * p.ldr + s] : -INFINITY;
+        const int64_t e = s < p.topk ? (int64_t)__ldcg(p.ids + row * p.ldr + s) : -1;
+        float v = e >= 0 ? __ldcg(p.wts + row * p.ldr + s) : -INFINITY;
         if (p.softmax) {
             float top = v;
 #pragma unroll
@@ -383,15 +491,21 @@ __global__ void __launch_bounds__(128) combine_kernel(const Params p) {
             v /= sum;
         }
         w[s] = v;
+        held[s] = e >= p.base && e - p.base < p.experts;
     }
     __syncthreads();
+    grid_dependency_wait();
     const int j = blockIdx.x * blockDim.x + threadIdx.x;
     if (j >= p.hidden) return;
     float y = 0.0f;
-    for (int s = 0; s < p.topk; ++s) {
-        const int64_t e = p.ids[row * p.ldr + s];
-        if (e < p.base || e - p.base >= p.experts) continue;
-        y = fmaf(w[s], p.down[(int64_t)(row * p.topk + s) * p.hidden + j], y);
+    for (int s0 = 0; s0 < p.topk; s0 += 8) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = s0 + i < p.topk && held[s0 + i] ? p.down[(int64_t)(row * p.topk + s0 + i) * p.hidden + j] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (s0 + i < p.topk && held[s0 + i]) y = fmaf(w[s0 + i], v[i], y);
     }
     if (p.out_bf16)
         static_cast<__nv_bfloat16 *>(p.Y)[row * p.ldy + j] = __float2bfloat16_rn(y);
@@ -399,8 +513,8 @@ __global__ void __launch_bounds__(128) combine_kernel(const Params p) {
         static_cast<float *>(p.Y)[row * p.ldy + j] = y;
 }
 
-cudaError_t launch_one(void (*kernel)(Params), dim3 grid, int threads, size_t smem, cudaStream_t stream,
-                       const Params &p) {
+template <class K>
+cudaError_t launch_one(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const Params &p) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
@@ -415,22 +529,89 @@ cudaError_t launch_one(void (*kernel)(Params), dim3 grid, int threads, size_t sm
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-size_t up_smem(const Params &p) {
-    return kChunkBytes + (size_t)p.m * row_stride(p.hidden) + (size_t)kWarps * p.stages * p.block;
+// Warps of a CTA and its shared memory.  Two CTAs of 8 warps share an SM where
+// the activations leave each 40 KB of ring; otherwise one CTA of 16 warps, or
+// of 8 where a bf16 ring (4 KB a block) leaves no room for 16.
+struct Plan {
+    int warps = 0, stages = 0;
+    size_t smem = 0;
+};
+
+Plan plan(size_t optin, size_t fixed, int length, int block, bool packed, int &per, int &slots) {
+    Plan out;
+    const size_t half = (optin + 1024) / 2 - 1024;
+    auto fits = [&](int warps, size_t limit, size_t ring) {
+        return fixed + 32 * warps + ring <= limit;
+    };
+    if (packed) {
+        out.warps = fits(8, half, 40 * 1024) ? 8 : 16;
+        const size_t limit = out.warps == 8 ? half : optin;
+        if (!fits(out.warps, limit, (size_t)2 * out.warps * block)) return Plan();
+        const int blocks = (int)((limit - fixed - 32 * out.warps) / out.warps / block);
+        per = std::min(length, blocks / 2);
+        slots = std::min(4, blocks / per);
+        out.smem = fixed + 32 * out.warps + (size_t)out.warps * slots * per * block;
+        return out;
+    }
+    per = 1;
+    const int tries[4][3] = {{8, 2, 0}, {16, 2, 1}, {8, 3, 1}, {8, 2, 1}};  // warps, stages, whole SM
+    for (const auto &c : tries)
+        if (fits(c[0], c[2] ? optin : half, (size_t)c[0] * c[1] * block)) {
+            out.warps = c[0];
+            out.stages = slots = c[1];
+            out.smem = fixed + 32 * c[0] + (size_t)c[0] * c[1] * block;
+            return out;
+        }
+    return out;
 }
-size_t down_smem(const Params &p) {
-    return kChunkBytes + (size_t)3 * p.cap * row_stride(p.inter) + (size_t)kWarps * p.stages * p.block;
+
+Plan up_plan(Params &p, size_t optin) {
+    const int kblocks = (p.hidden + kBlockK - 1) / kBlockK;
+    return plan(optin, kChunkBytes + (size_t)(p.m + 1) * row_stride(p.hidden), (kblocks + kSplit - 1) / kSplit,
+                p.block, p.fmt != 0, p.per_up, p.slots_up);
+}
+Plan down_plan(Params &p, size_t optin) {
+    const int kblocks = (p.inter + kBlockK - 1) / kBlockK;
+    return plan(optin, kChunkBytes + (size_t)(3 * p.cap + 1) * row_stride(p.inter), kblocks, p.block,
+                p.fmt != 0, p.per_down, p.slots_down);
+}
+
+dim3 grid_of(const Plan &pl) {
+    const bool two = pl.warps == 8 && 2 * (pl.smem + 1024) <= (size_t)mr_host::max_smem_optin() + 1024;
+    return dim3((unsigned)(mr_host::sm_count() * (two ? 2 : 1)));
+}
+
+template <int G, int WARPS, int STAGES>
+cudaError_t launch_up(const Params &p, const Plan &pl, cudaStream_t stream) {
+    static std::atomic<uint64_t> ready{0};
+    if (!allow_smem(up_kernel<G, WARPS, STAGES>, ready)) return cudaErrorInvalidValue;
+    return launch_one(up_kernel<G, WARPS, STAGES>, grid_of(pl),
+                      WARPS * 32, pl.smem, stream, p);
+}
+template <int G, int WARPS, int STAGES>
+cudaError_t launch_down(const Params &p, const Plan &pl, cudaStream_t stream) {
+    static std::atomic<uint64_t> ready{0};
+    if (!allow_smem(down_kernel<G, WARPS, STAGES>, ready)) return cudaErrorInvalidValue;
+    return launch_one(down_kernel<G, WARPS, STAGES>, grid_of(pl),
+                      WARPS * 32, pl.smem, stream, p);
 }
 
 template <int G>
-mr_status launch(const Params &p, cudaStream_t stream) {
-    static std::atomic<uint64_t> ready_up{0}, ready_down{0};
-    if (!allow_smem(up_kernel<G>, ready_up) || !allow_smem(down_kernel<G>, ready_down)) return MR_ERR_CUDA;
-    const int sms = mr_host::sm_count();
-    const size_t sm_bytes = (size_t)mr_host::max_smem_optin() + 1024, fixed = 1024;
-    auto grid = [&](size_t smem) { return dim3((unsigned)(sms * (2 * (smem + fixed) <= sm_bytes ? 2 : 1))); };
-    cudaError_t e = launch_one(up_kernel<G>, grid(up_smem(p)), kThreads, up_smem(p), stream, p);
-    if (e == cudaSuccess) e = launch_one(down_kernel<G>, grid(down_smem(p)), kThreads, down_smem(p), stream, p);
+mr_status launch(const Params &p, const Plan &up, const Plan &down, cudaStream_t stream) {
+    cudaError_t e;
+    if constexpr (G) {
+        e = up.warps == 8 ? launch_up<G, 8, 0>(p, up, stream) : launch_up<G, 16, 0>(p, up, stream);
+        if (e == cudaSuccess)
+            e = down.warps == 8 ? launch_down<G, 8, 0>(p, down, stream) : launch_down<G, 16, 0>(p, down, stream);
+    } else {
+        e = up.warps == 16   ? launch_up<0, 16, 2>(p, up, stream)
+            : up.stages == 3 ? launch_up<0, 8, 3>(p, up, stream)
+                             : launch_up<0, 8, 2>(p, up, stream);
+        if (e == cudaSuccess)
+            e = down.warps == 16   ? launch_down<0, 16, 2>(p, down, stream)
+                : down.stages == 3 ? launch_down<0, 8, 3>(p, down, stream)
+                                   : launch_down<0, 8, 2>(p, down, stream);
+    }
     if (e == cudaSuccess)
         e = launch_one(combine_kernel, dim3((unsigned)((p.hidden + 127) / 128), (unsigned)p.m), 128, 0, stream, p);
     return mr_host::cuda_status(e);
@@ -461,23 +642,24 @@ mr_status run(Params p, int out_dtype, uint32_t flags, void *workspace, size_t w
     if (p.hidden % 8 || p.inter % 8) return MR_ERR_MISALIGNED;
     if (!sizes_supported(p.m, p.topk, p.hidden, p.inter)) return MR_ERR_UNSUPPORTED;
     if (workspace_bytes < moe_window_workspace_bytes(p.m, p.topk, p.hidden, p.inter)) return MR_ERR_INVALID_ARG;
-    p.part = static_cast<float *>(workspace);
-    p.down = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + part_bytes(p.m, p.topk, p.inter));
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.part = reinterpret_cast<float *>(ws);
+    p.down = reinterpret_cast<float *>(ws + part_bytes(p.m, p.topk, p.inter));
     p.cap = std::min(kChunk, p.m);
     p.out_bf16 = out_dtype == MR_BF16;
     p.softmax = (flags & MR_MOE_SOFTMAX) != 0;
-    const int G = (int)(p.fmt & MR_W4_GROUP_MASK);
-    p.block = G ? block_bytes(p.fmt) : kBlockBf16;
-    p.stages = G ? 8 : 2;
+    p.block = p.fmt ? block_bytes(p.fmt) : kBlockBf16;
     const int optin = mr_host::max_smem_optin();
-    const size_t most = std::max(up_smem(p), down_smem(p));
-    if (most > (size_t)(optin > 0 ? optin : 232448)) return MR_ERR_UNSUPPORTED;
+    const size_t most = (size_t)(optin > 0 ? optin : 232448);
+    const Plan up = up_plan(p, most), down = down_plan(p, most);
+    if (!up.warps || !down.warps) return MR_ERR_UNSUPPORTED;
     if (optin <= 0) return MR_ERR_CUDA;
-    switch (G) {
-        case 0: return launch<0>(p, stream);
-        case 32: return launch<32>(p, stream);
-        case 64: return launch<64>(p, stream);
-        default: return launch<128>(p, stream);
+    p.up_warps = (int)grid_of(up).x * up.warps;
+    switch (p.fmt & MR_W4_GROUP_MASK) {
+        case 0: return launch<0>(p, up, down, stream);
+        case 32: return launch<32>(p, up, down, stream);
+        case 64: return launch<64>(p, up, down, stream);
+        default: return launch<128>(p, up, down, stream);
     }
 }
 

@@ -62,9 +62,9 @@ __global__ void __launch_bounds__(256) pack_kernel(const uint8_t *__restrict__ q
             }
             *reinterpret_cast<uint4 *>(out + 512 * h + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        for (int e = lane; e < per_block * kTileRows; e += 32) {
-            const int64_t row = source_row(e % kTileRows);
-            const int grp = kb * per_block + e / kTileRows;
+        for (int e = lane; e < per_block * kTileRows; e += 32) {  // [g][half][group]
+            const int64_t row = source_row(e / (2 * per_block) + 8 * (e / per_block % 2));
+            const int grp = kb * per_block + e % per_block;
             const bool in = row >= 0 && grp < groups;
             reinterpret_cast<uint16_t *>(out + kBlockQ)[e] = in ? scales[row * groups + grp] : (uint16_t)0;
             if (fmt & MR_W4_ZEROS)
@@ -77,11 +77,7 @@ __global__ void __launch_bounds__(256) pack_kernel(const uint8_t *__restrict__ q
 
 constexpr int kMaxRows = 16;
 constexpr int kMaxK = 1 << 20;               // far beyond what shared memory holds
-constexpr int kWarps = 8;
 constexpr int kKW = 4;                       // warps that share a tile
-constexpr int kWorkers = kWarps / kKW;
-constexpr int kRedCol = 20;                  // floats between columns of a partial tile (no bank conflicts)
-constexpr int kStages = 4;
 
 struct Params {
     const uint8_t *A;
@@ -90,114 +86,147 @@ struct Params {
     float *C;
     int64_t ldc;
     int m, n, k, tiles, kblocks, block;
+    int per, slots;    // blocks of a ring stage, stages of a warp's ring
     uint32_t fmt;
 };
 
-__host__ __device__ inline int x_stride(int kblocks) { return kblocks * kBlockK * 2 + 64; }  // odd multiple of 64
-__host__ __device__ constexpr int red_floats(int NT) { return kWorkers * 2 * kKW * 8 * NT * kRedCol; }
+// Bytes between activation rows in shared memory: an odd multiple of 64, so
+// that the eight 16-byte pieces of a load phase (two rows) miss no bank twice.
+__host__ __device__ inline int64_t x_stride(int kblocks) { return (int64_t)kblocks * kBlockK * 2 + 64; }
+// The quarters of a tile on their way to the first warp: two buffers of three.
+__host__ __device__ constexpr int red_bytes(int warps, int NT) { return warps / kKW * 2 * (kKW - 1) * NT * 512; }
 
-inline size_t smem_bytes(int m, int kblocks, int block) {
-    return (size_t)m * x_stride(kblocks) + (size_t)kWarps * kStages * block +
-           sizeof(float) * red_floats(m > 8 ? 2 : 1);
-}
-
-template <int G, bool F16, int NT>
-__global__ void __launch_bounds__(kWarps * 32, 2) gemv_kernel(const Params p) {
+template <int G, bool F16, int NT, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) gemv_kernel(const Params p) {
     extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int kWorkers = WARPS / kKW;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int worker = warp / kKW, slice = warp % kKW, g = lane >> 2, t = lane & 3;
-    const int xs = x_stride(p.kblocks);
-    const uint32_t x0 = smem_u32(smem);
-    const uint32_t ring = x0 + p.m * xs + warp * kStages * p.block;
-    float *red = reinterpret_cast<float *>(smem + p.m * xs + kWarps * kStages * p.block) +
-                 worker * 2 * kKW * 8 * NT * kRedCol;
+    const int xs = (int)x_stride(p.kblocks), x_bytes = (p.m + 1) * xs;
+    const uint32_t x0 = smem_u32(smem), red = x0 + x_bytes + worker * 2 * (kKW - 1) * NT * 512;
+    const uint32_t ring0 = x0 + x_bytes + red_bytes(WARPS, NT);
+    const int ring_bytes = p.slots * p.per * p.block;
+    Ring ring(ring0 + warp * ring_bytes, ring0 + WARPS * ring_bytes + warp * p.slots * 8, p.slots, p.per * p.block);
     grid_launch_dependents();
+    ring.init(lane);
 
     // This warp's blocks: its quarter [kb0, kb1) of tile first, first + step, ...
     const int kb0 = p.kblocks * slice / kKW, kb1 = p.kblocks * (slice + 1) / kKW;
     const int first = blockIdx.x * kWorkers + worker, step = gridDim.x * kWorkers;
-    int itile = first, ikb = kb0;  // the next block to request
-    auto request = [&](int stage) {
-        if (itile < p.tiles && kb0 < kb1) {
-            issue_block(ring + stage * p.block, p.W + ((int64_t)itile * p.kblocks + ikb) * p.block, p.block, lane);
-            if (++ikb == kb1) {
-                ikb = kb0;
-                itile += step;
-            }
+    int itile = kb0 < kb1 ? first : p.tiles, ikb = kb0;  // the next blocks to request
+    auto request = [&]() {
+        if (itile >= p.tiles) return;
+        const int count = min(p.per, kb1 - ikb);
+        ring.request(p.W + ((int64_t)itile * p.kblocks + ikb) * p.block, count * p.block, lane);
+        ikb += count;
+        if (ikb == kb1) {
+            ikb = kb0;
+            itile += step;
         }
-        cp_async_commit();
     };
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) request(s);
+    for (int s = 0; s < p.slots; ++s) request();
 
     // The weight streams while the activations' producer finishes.
     grid_dependency_wait();
     const int chunks = p.kblocks * (kBlockK / 8), live = p.k / 8;
-    for (int e = threadIdx.x; e < p.m * chunks; e += kWarps * 32) {
-        const int r = e / chunks, c = e % chunks;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (c < live) v = *reinterpret_cast<const uint4 *>(p.A + r * p.lda + 16 * c);
-        *reinterpret_cast<uint4 *>(smem + r * xs + 16 * c) = v;
-    }
+    for (int r = warp; r <= p.m; r += WARPS)
+        for (int c = lane; c < chunks; c += 32) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (r < p.m && c < live) v = *reinterpret_cast<const uint4 *>(p.A + r * p.lda + 16 * c);
+            *reinterpret_cast<uint4 *>(smem + r * xs + 16 * c) = v;
+        }
     __syncthreads();
 
-    bool on[NT];
     uint32_t xb[NT];
 #pragma unroll
-    for (int c = 0; c < NT; ++c) {
-        on[c] = 8 * c + g < p.m;
-        xb[c] = x0 + (on[c] ? 8 * c + g : 0) * xs + 16 * t;
-    }
-    int stage = 0, buf = 0;
+    for (int c = 0; c < NT; ++c) xb[c] = x0 + min(8 * c + g, p.m) * xs + 16 * t;
+    int buf = 0;
     for (int tile = first; tile < p.tiles; tile += step) {
         float C[NT][4] = {};
-        for (int kb = kb0; kb < kb1; ++kb) {
-            cp_async_wait<kStages - 1>();
-            __syncwarp();  // every lane's part of the block has arrived
-            uint32_t x[NT];
+        for (int kb = kb0; kb < kb1; kb += p.per) {
+            const uint32_t at = ring.wait();
+            const int count = min(p.per, kb1 - kb);
+#pragma unroll 2
+            for (int b = 0; b < count; ++b) {
+                uint32_t x[NT];
 #pragma unroll
-            for (int c = 0; c < NT; ++c) x[c] = xb[c] + kb * (kBlockK * 2);
-            consume_block<G, F16, NT>(ring + stage * p.block, p.fmt, x, on, C, lane);
-            __syncwarp();  // every lane has read it
-            request(stage);
-            stage = stage + 1 == kStages ? 0 : stage + 1;
+                for (int c = 0; c < NT; ++c) x[c] = xb[c] + (kb + b) * (kBlockK * 2);
+                consume_block<G, F16, NT>(at + b * p.block, p.fmt, x, C, lane);
+            }
+            ring.done();
+            request();
         }
-        // Quarters in order.  Two buffers: a warp writes buffer b again only
-        // after the barrier of the tile between, which the others reach after
-        // reading b.
-        float *mine = red + (buf * kKW + slice) * 8 * NT * kRedCol;
+        // The first warp adds the quarters in order.  Two buffers: a warp
+        // writes one again only after the barrier of the tile between, which
+        // the first warp reaches after reading it.
+        const uint32_t part = red + buf * (kKW - 1) * NT * 512 + 16 * lane;
+        if (slice) {
 #pragma unroll
-        for (int c = 0; c < NT; ++c) {
-            mine[(8 * c + 2 * t) * kRedCol + g] = C[c][0];
-            mine[(8 * c + 2 * t + 1) * kRedCol + g] = C[c][1];
-            mine[(8 * c + 2 * t) * kRedCol + g + 8] = C[c][2];
-            mine[(8 * c + 2 * t + 1) * kRedCol + g + 8] = C[c][3];
+            for (int c = 0; c < NT; ++c)
+                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(part + ((slice - 1) * NT + c) * 512),
+                             "f"(C[c][0]), "f"(C[c][1]), "f"(C[c][2]), "f"(C[c][3])
+                             : "memory");
         }
         asm volatile("bar.sync %0, %1;" ::"r"(1 + worker), "n"(kKW * 32) : "memory");
+        if (slice == 0) {
 #pragma unroll
-        for (int c = 0; c < NT; ++c) {
-            const int col = 8 * c + (threadIdx.x % (kKW * 32)) / kTileRows, r = threadIdx.x % kTileRows;
-            const float *from = red + buf * kKW * 8 * NT * kRedCol + col * kRedCol + r;
-            float sum = from[0];
+            for (int s = 0; s < kKW - 1; ++s)
 #pragma unroll
-            for (int s = 1; s < kKW; ++s) sum += from[s * 8 * NT * kRedCol];
-            const int row = tile * kTileRows + r;
-            if (col < p.m && row < p.n) p.C[col * p.ldc + row] = sum;
+                for (int c = 0; c < NT; ++c) {
+                    const uint4 v = lds128(part + (s * NT + c) * 512);
+                    C[c][0] += __uint_as_float(v.x);
+                    C[c][1] += __uint_as_float(v.y);
+                    C[c][2] += __uint_as_float(v.z);
+                    C[c][3] += __uint_as_float(v.w);
+                }
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int col = 8 * c + 2 * t + (e & 1), row = tile * kTileRows + g + 8 * (e >> 1);
+                    if (col < p.m && row < p.n) p.C[col * p.ldc + row] = C[c][e];
+                }
         }
         buf ^= 1;
     }
 }
 
-template <int G, bool F16, int NT>
-mr_status launch(const Params &p, size_t smem, uint32_t flags, cudaStream_t stream) {
+// Shared memory and the launch's shape.  Two CTAs of 8 warps share an SM when
+// the activations leave each of them 40 KB of ring (the next launch's CTA then
+// also finds room under programmatic launch); otherwise one of 16 warps.  A
+// stage holds a warp's whole quarter of a tile where two of them fit.
+struct Plan {
+    int warps = 0;
+    size_t smem = 0;
+};
+
+Plan plan(Params &p, size_t optin) {
+    Plan out;
+    const int NT = p.m > 8 ? 2 : 1, quarter = (p.kblocks + kKW - 1) / kKW;
+    for (int warps : {8, 16}) {
+        const size_t limit = warps == 8 ? (optin + 1024) / 2 - 1024 : optin;
+        const size_t fixed = (size_t)(p.m + 1) * x_stride(p.kblocks) + red_bytes(warps, NT) + 8 * 4 * warps;
+        if (fixed + (warps == 8 ? 40 * 1024 : 2 * warps * p.block) > limit) continue;
+        const int blocks = (int)((limit - fixed) / warps / p.block);  // a warp's ring, at least 2
+        p.per = std::min(quarter, blocks / 2);
+        p.slots = std::min(4, blocks / p.per);
+        out.warps = warps;
+        out.smem = fixed + (size_t)warps * p.slots * p.per * p.block;
+        return out;
+    }
+    return out;
+}
+
+template <int G, bool F16, int NT, int WARPS>
+mr_status launch(const Params &p, const Plan &pl, uint32_t flags, cudaStream_t stream) {
     static std::atomic<uint64_t> ready{0};
-    auto kernel = gemv_kernel<G, F16, NT>;
+    auto kernel = gemv_kernel<G, F16, NT, WARPS>;
     if (!allow_smem(kernel, ready)) return MR_ERR_CUDA;
+    constexpr int kWorkers = WARPS / kKW;
     cudaLaunchConfig_t cfg = {};
-    const int per_sm = 2 * (smem + 1024) <= (size_t)mr_host::max_smem_optin() + 1024 ? 2 : 1;
-    cfg.gridDim = dim3((unsigned)std::min((p.tiles + kWorkers - 1) / kWorkers, mr_host::sm_count() * per_sm));
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.dynamicSmemBytes = smem;
+    cfg.gridDim = dim3((unsigned)std::min((p.tiles + kWorkers - 1) / kWorkers, mr_host::sm_count() * (16 / WARPS)));
+    cfg.blockDim = dim3(WARPS * 32);
+    cfg.dynamicSmemBytes = pl.smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -207,10 +236,16 @@ mr_status launch(const Params &p, size_t smem, uint32_t flags, cudaStream_t stre
     return mr_host::cuda_status(cudaLaunchKernelEx(&cfg, kernel, p));
 }
 
+template <int G, bool F16>
+mr_status launch_rows(const Params &p, const Plan &pl, uint32_t flags, cudaStream_t stream) {
+    if (p.m > 8)
+        return pl.warps == 8 ? launch<G, F16, 2, 8>(p, pl, flags, stream) : launch<G, F16, 2, 16>(p, pl, flags, stream);
+    return pl.warps == 8 ? launch<G, F16, 1, 8>(p, pl, flags, stream) : launch<G, F16, 1, 16>(p, pl, flags, stream);
+}
+
 template <int G>
-mr_status launch_group(const Params &p, bool f16, size_t smem, uint32_t flags, cudaStream_t stream) {
-    if (f16) return p.m > 8 ? launch<G, true, 2>(p, smem, flags, stream) : launch<G, true, 1>(p, smem, flags, stream);
-    return p.m > 8 ? launch<G, false, 2>(p, smem, flags, stream) : launch<G, false, 1>(p, smem, flags, stream);
+mr_status launch_group(const Params &p, const Plan &pl, bool f16, uint32_t flags, cudaStream_t stream) {
+    return f16 ? launch_rows<G, true>(p, pl, flags, stream) : launch_rows<G, false>(p, pl, flags, stream);
 }
 
 // MR_OK, or why a weight of n x k cannot be packed in this format.
@@ -280,15 +315,15 @@ extern "C" mr_status mrgemv_w4(const void *A, int64_t lda, const void *packed, s
     p.kblocks = mr::w4::kblocks_of(k);
     p.block = mr::w4::block_bytes(fmt);
     p.fmt = fmt;
-    const size_t smem = mr::w4::smem_bytes(m, p.kblocks, p.block);
     const int optin = mr_host::max_smem_optin();
-    if (smem > (size_t)(optin > 0 ? optin : 232448)) return MR_ERR_UNSUPPORTED;
+    const mr::w4::Plan pl = mr::w4::plan(p, (size_t)(optin > 0 ? optin : 232448));
+    if (!pl.warps) return MR_ERR_UNSUPPORTED;
     if (optin <= 0) return MR_ERR_CUDA;
     const bool f16 = in_dtype == MR_F16;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (fmt & MR_W4_GROUP_MASK) {
-        case 32: return mr::w4::launch_group<32>(p, f16, smem, flags, s);
-        case 64: return mr::w4::launch_group<64>(p, f16, smem, flags, s);
-        default: return mr::w4::launch_group<128>(p, f16, smem, flags, s);
+        case 32: return mr::w4::launch_group<32>(p, pl, f16, flags, s);
+        case 64: return mr::w4::launch_group<64>(p, pl, f16, flags, s);
+        default: return mr::w4::launch_group<128>(p, pl, f16, flags, s);
     }
 }

@@ -66,39 +66,60 @@ template <bool F16>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
     if constexpr (F16)
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
             "{%0, %1, %2, %3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
             "{%0, %1, %2, %3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// d = a . b
+template <bool F16>
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+    if constexpr (F16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // ---- 4-bit values ---------------------------------------------------------
 
 // One word holds 8 values: nibble i is value 2i, nibble 4 + i is value 2i + 1.
 // Pair i is (q - z) of both, exact: the nibble is put into the low mantissa
-// bits of 128 (bf16) or 1024 (f16), whose spacing is 1 there, and 128 + z or
-// 1024 + z (`zero`, both halves) is subtracted.
+// bits of 128 (bf16) or 1024 (f16), whose spacing is 1 there, and -(128 + z)
+// or -(1024 + z) (`minus`, both halves) is added.
+// `one` is 128 or 1024 in both halves, kept in a register by `magic`: with mask
+// and constant both known, the compiler emits two logic operations for the one.
 template <bool F16>
-__device__ __forceinline__ uint32_t pair(uint32_t word, int i, uint32_t zero) {
-    const uint32_t v = ((word >> (4 * i)) & 0x000F000Fu) | (F16 ? 0x64006400u : 0x43004300u);
-    uint32_t r;
+__device__ __forceinline__ uint32_t magic(uint32_t fmt) {
+    return (F16 ? 0x64006400u : 0x43004300u) + (fmt >> 31);  // no format has bit 31
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pair(uint32_t word, int i, uint32_t one, uint32_t minus) {
+    uint32_t v, r;
+    asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(v) : "r"(word >> (4 * i)), "r"(one));
     if constexpr (F16)
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(zero));
+        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(minus));
     else
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(zero));
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0x3F803F80u), "r"(minus));
     return r;
 }
 
 template <bool F16>
-__device__ __forceinline__ uint32_t zero_pair(uint32_t z) {
-    return z * 0x00010001u + (F16 ? 0x64006400u : 0x43004300u);
+__device__ __forceinline__ uint32_t minus_zero(uint32_t z) {
+    return z * 0x00010001u + (F16 ? 0xE400E400u : 0xC300C300u);
 }
 
 // A stored 16-bit scale in fp32 (exact).
@@ -106,74 +127,104 @@ __device__ __forceinline__ float scale_value(uint16_t bits, bool f16) {
     return f16 ? __half2float(__ushort_as_half(bits)) : __uint_as_float((uint32_t)bits << 16);
 }
 
-__device__ __forceinline__ uint16_t lds_u16(uint32_t addr) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-
-// Request one packed block into `stage` (asynchronous; the caller commits).
-__device__ __forceinline__ void issue_block(uint32_t stage, const uint8_t *src, int bytes, int lane) {
-    cp_async16(stage + 16 * lane, src + 16 * lane);
-    cp_async16(stage + 512 + 16 * lane, src + 512 + 16 * lane);
-    if (kBlockQ + 16 * lane < bytes) cp_async16(stage + kBlockQ + 16 * lane, src + kBlockQ + 16 * lane);
-}
+template <int BYTES>
+struct Word;
+template <>
+struct Word<2> {
+    static __device__ __forceinline__ void read(uint32_t addr, uint32_t (&w)[1]) {
+        uint16_t v;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+        w[0] = v;
+    }
+};
+template <>
+struct Word<4> {
+    static __device__ __forceinline__ void read(uint32_t addr, uint32_t (&w)[1]) {
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+    }
+};
+template <>
+struct Word<8> {
+    static __device__ __forceinline__ void read(uint32_t addr, uint32_t (&w)[2]) {
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+    }
+};
+template <>
+struct Word<16> {
+    static __device__ __forceinline__ void read(uint32_t addr, uint32_t (&w)[4]) {
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(addr)
+                     : "memory");
+    }
+};
 
 // C += (one packed block) . (the activation columns).  x[c] is the shared
 // address of this lane's 16 bytes of column g of column tile c at the block's
-// first k, on[c] whether that column exists.  The values of a group are
-// summed by the tensor core as small exact integers times the activations
-// and take their scale once, in fp32: the sum of at most 128 products is the
-// longest chain of the matrix instruction's own additions, which round
-// towards zero, so its error does not grow with k.
+// first k (a row of zeros where that column does not exist).  The values of a
+// group are summed by the tensor core as small exact integers times the
+// activations and take their scale once, in fp32: the sum of at most 128
+// products is the longest chain of the matrix instruction's own additions,
+// which round towards zero, so its error does not grow with k.
+//
+// What bounds it is the ALU pipe: 7 shifts and masks for 8 values, 56 of the
+// about 115 instructions a block costs at NT = 1; at the HBM rate a block has
+// 44 cycles of an SM, 88 slots of that pipe.  A group of 128 runs as two chains of
+// four instructions instead of one of eight.
 template <int G, bool F16, int NT>
 __device__ __forceinline__ void consume_block(uint32_t stage, uint32_t fmt, const uint32_t (&x)[NT],
-                                              const bool (&on)[NT], float (&C)[NT][4], int lane) {
+                                              float (&C)[NT][4], int lane) {
+    constexpr int kGroups = kBlockK / G, kChains = G >= 128 ? 2 : 1;
     const int g = lane >> 2;
+    const uint32_t one = magic<F16>(fmt);
     const uint4 v0 = lds128(stage + 16 * lane), v8 = lds128(stage + 512 + 16 * lane);
     const uint32_t q0[4] = {v0.x, v0.y, v0.z, v0.w}, q8[4] = {v8.x, v8.y, v8.z, v8.w};
+    // scales and zero points of rows g and g + 8, one read each
+    uint32_t sw[kGroups], zw[(kGroups + 1) / 2];
+    Word<4 * kGroups>::read(stage + kBlockQ + 4 * kGroups * g, sw);
     const bool sf16 = (fmt & MR_W4_SCALE_F16) != 0, zeros = (fmt & MR_W4_ZEROS) != 0;
-    constexpr int kGroups = kBlockK / G;
-    const uint32_t scales = stage + kBlockQ, zs = scales + 32 * kGroups;
+    if (zeros) Word<2 * kGroups>::read(stage + kBlockQ + 32 * kGroups + 2 * kGroups * g, zw);
+    auto scale_of = [&](int i) {  // i: half * kGroups + group
+        return scale_value((uint16_t)(sw[i / 2] >> (16 * (i & 1))), sf16);
+    };
+    auto zero_of = [&](int i) { return minus_zero<F16>((zw[i / 4] >> (8 * (i & 3))) & 0xFFu); };
 #pragma unroll
     for (int gi = 0; gi < kGroups; ++gi) {
-        uint32_t z0 = zero_pair<F16>(8u), z8 = z0;
+        uint32_t z0 = minus_zero<F16>(8u), z8 = z0;
         if (zeros) {
-            z0 = zero_pair<F16>(lds_u8(zs + 16 * gi + g));
-            z8 = zero_pair<F16>(lds_u8(zs + 16 * gi + g + 8));
+            z0 = zero_of(gi);
+            z8 = zero_of(kGroups + gi);
         }
-        float acc[NT][4] = {};
+        float acc[kChains][NT][4];
 #pragma unroll
         for (int j = gi * (G / 32); j < (gi + 1) * (G / 32); ++j) {
             uint32_t a0[4], a8[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                a0[i] = pair<F16>(q0[j], i, z0);
-                a8[i] = pair<F16>(q8[j], i, z8);
+                a0[i] = pair<F16>(q0[j], i, one, z0);
+                a8[i] = pair<F16>(q8[j], i, one, z8);
             }
 #pragma unroll
             for (int c = 0; c < NT; ++c) {
-                uint4 b = make_uint4(0, 0, 0, 0);
-                if (on[c]) b = lds128(x[c] + 64 * j);
-                mma<F16>(acc[c], a0[0], a8[0], a0[1], a8[1], b.x, b.y);
-                mma<F16>(acc[c], a0[2], a8[2], a0[3], a8[3], b.z, b.w);
+                const uint4 b = lds128(x[c] + 64 * j);
+                if (j == gi * (G / 32))
+                    mma_first<F16>(acc[0][c], a0[0], a8[0], a0[1], a8[1], b.x, b.y);
+                else
+                    mma<F16>(acc[0][c], a0[0], a8[0], a0[1], a8[1], b.x, b.y);
+                if (kChains > 1 && j == gi * (G / 32))
+                    mma_first<F16>(acc[kChains - 1][c], a0[2], a8[2], a0[3], a8[3], b.z, b.w);
+                else
+                    mma<F16>(acc[kChains - 1][c], a0[2], a8[2], a0[3], a8[3], b.z, b.w);
             }
         }
-        const float s0 = scale_value(lds_u16(scales + 32 * gi + 2 * g), sf16);
-        const float s8 = scale_value(lds_u16(scales + 32 * gi + 2 * g + 16), sf16);
+        const float s0 = scale_of(gi), s8 = scale_of(kGroups + gi);
 #pragma unroll
-        for (int c = 0; c < NT; ++c) {
-            C[c][0] = fmaf(s0, acc[c][0], C[c][0]);
-            C[c][1] = fmaf(s0, acc[c][1], C[c][1]);
-            C[c][2] = fmaf(s8, acc[c][2], C[c][2]);
-            C[c][3] = fmaf(s8, acc[c][3], C[c][3]);
-        }
+        for (int c = 0; c < NT; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float sum = kChains > 1 ? acc[0][c][e] + acc[kChains - 1][c][e] : acc[0][c][e];
+                C[c][e] = fmaf(e < 2 ? s0 : s8, sum, C[c][e]);
+            }
     }
 }
 
@@ -199,26 +250,71 @@ __device__ __forceinline__ void issue_block_bf16(uint32_t stage, const uint16_t 
 // C += (the block) . (the activation columns); the tensor core's own sums end
 // with the block, as in consume_block.
 template <int NT>
-__device__ __forceinline__ void consume_block_bf16(uint32_t stage, const uint32_t (&x)[NT], const bool (&on)[NT],
-                                                   float (&C)[NT][4], int lane) {
-    float acc[NT][4] = {};
+__device__ __forceinline__ void consume_block_bf16(uint32_t stage, const uint32_t (&x)[NT], float (&C)[NT][4],
+                                                   int lane) {
+    float acc[2][NT][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const uint4 v0 = lds128(stage + (2 * j) * 512 + 16 * lane);
         const uint4 v8 = lds128(stage + (2 * j + 1) * 512 + 16 * lane);
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
-            uint4 b = make_uint4(0, 0, 0, 0);
-            if (on[c]) b = lds128(x[c] + 64 * j);
-            mma<false>(acc[c], v0.x, v8.x, v0.y, v8.y, b.x, b.y);
-            mma<false>(acc[c], v0.z, v8.z, v0.w, v8.w, b.z, b.w);
+            const uint4 b = lds128(x[c] + 64 * j);
+            if (j == 0) {
+                mma_first<false>(acc[0][c], v0.x, v8.x, v0.y, v8.y, b.x, b.y);
+                mma_first<false>(acc[1][c], v0.z, v8.z, v0.w, v8.w, b.z, b.w);
+            } else {
+                mma<false>(acc[0][c], v0.x, v8.x, v0.y, v8.y, b.x, b.y);
+                mma<false>(acc[1][c], v0.z, v8.z, v0.w, v8.w, b.z, b.w);
+            }
         }
     }
 #pragma unroll
     for (int c = 0; c < NT; ++c)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) C[c][i] += acc[c][i];
+        for (int i = 0; i < 4; ++i) C[c][i] += acc[0][c][i] + acc[1][c][i];
 }
+
+// ---- a warp's ring of packed blocks ---------------------------------------
+
+// `slots` stages of up to `per` consecutive blocks, each filled by one bulk copy
+// that lane 0 requests and an mbarrier counts.  Requests and takes go through
+// the stages in the same order; a stage is requested again only after every
+// lane has read it (__syncwarp), so a wait is never more than one phase ahead.
+struct Ring {
+    uint32_t data, bars;
+    int slots, stage_bytes;
+    int put_at = 0, take_at = 0;
+    uint32_t parity = 0;
+    bool dead = false;  // a wait ran out: later ones are not tried
+    __device__ __forceinline__ Ring(uint32_t d, uint32_t b, int n, int bytes)
+        : data(d), bars(b), slots(n), stage_bytes(bytes) {}
+    __device__ __forceinline__ void init(int lane) const {
+        if (lane == 0) {
+            for (int i = 0; i < slots; ++i) mbar_init(bars + 8 * i, 1);
+            fence_mbar_init();
+        }
+        __syncwarp();
+    }
+    __device__ __forceinline__ void request(const uint8_t *src, int bytes, int lane) {
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bars + 8 * put_at, (uint32_t)bytes);
+            bulk_g2s(data + put_at * stage_bytes, src, (uint32_t)bytes, bars + 8 * put_at);
+        }
+        put_at = put_at + 1 == slots ? 0 : put_at + 1;
+    }
+    __device__ __forceinline__ uint32_t wait() {  // the next stage, once its bytes have arrived
+        if (!dead) dead = !mbar_wait_bounded(bars + 8 * take_at, parity, MR_DEVERR_GEMV_TIMEOUT);
+        return data + take_at * stage_bytes;
+    }
+    __device__ __forceinline__ void done() {  // this lane has read the stage
+        __syncwarp();
+        if (++take_at == slots) {
+            take_at = 0;
+            parity ^= 1u;
+        }
+    }
+};
 
 // Allow `kernel` all the shared memory the device offers, once per device.
 template <class K>
