@@ -38,7 +38,7 @@ constexpr int kMaxRows = 16;
 constexpr int kMaxTopk = 32;
 constexpr int kMaxSlots = kMaxRows * kMaxTopk;
 constexpr int kChunk = 8;        // choices of one expert that share a pass over its weight
-constexpr int kSplit = 4;        // parts of k in the up projection
+constexpr int kSplit = kKW;      // parts of k in the up projection
 
 struct Params {
     const uint8_t *X;
@@ -141,10 +141,9 @@ __host__ __device__ inline int row_stride(int k) { return (k + kBlockK - 1) / kB
 // lane copies the bytes it reads itself.
 
 // Whether a warp of the up kernel sums all quarters of a tile itself: when
-// that still gives every warp four tiles (8 rows of 4-bit experts, 6000 tiles,
-// 2368 warps: quarters; 16 rows: whole tiles).
+// that still gives every warp two tiles.
 __device__ __forceinline__ bool whole_tiles(const Params &p, int chunks) {
-    return chunks * (p.inter / 8) >= 4 * p.up_warps;
+    return chunks * (p.inter / 8) >= 2 * p.up_warps;
 }
 
 // ---- up projection --------------------------------------------------------
@@ -181,32 +180,36 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) up_kernel(const Params
     const int64_t items = (int64_t)(chunks.n * tiles) << shift;
     const int i0 = (int)(items * blockIdx.x / gridDim.x) + warp, i1 = (int)(items * (blockIdx.x + 1) / gridDim.x);
     const int slice = whole ? 0 : i0 & 3, step = WARPS >> shift;
-    const int kb0 = kblocks * slice / kSplit, kb1 = whole ? kblocks : kblocks * (slice + 1) / kSplit;
     int left = i0 < i1 ? (i1 - i0 + WARPS - 1) / WARPS : 0;  // items of this warp
     int chunk = (i0 >> shift) / tiles, tile = (i0 >> shift) % tiles;
 
     // the next blocks to request
+    const int kb0 = quarter_begin(kblocks, slice), kb1 = whole ? kblocks : quarter_begin(kblocks, slice + 1);
     int rleft = kb0 < kb1 ? left : 0, rchunk = chunk, rtile = tile, rkb = kb0;
     const uint8_t *src0 = nullptr, *src8 = nullptr;
     auto aim = [&]() {
         const uint8_t *w = p.Wu + (int64_t)chunks.expert[rchunk] * p.eu;
         if (G) {
-            src0 = w + (int64_t)(rtile * kblocks) * p.block;
+            src0 = w + (int64_t)(rtile * kblocks + kb0) * p.block;
         } else {
-            src0 = w + (int64_t)(rtile * 8 + g) * p.ldu;
+            src0 = w + (int64_t)(rtile * 8 + g) * p.ldu + kb0 * kBlockK * 2;
             src8 = src0 + (int64_t)p.inter * p.ldu;
         }
     };
     if (rleft) aim();
-    auto request = [&](int stage) {
+    int rstage = 0;  // bf16: the stage of the next request
+    auto request = [&]() {
         if (rleft) {
             const int count = G ? min(p.per_up, kb1 - rkb) : 1;
-            if (G)
-                ring.request(src0 + rkb * p.block, count * p.block, lane);
-            else
-                issue_block_bf16(ring.data + stage * p.block, reinterpret_cast<const uint16_t *>(src0) + rkb * kBlockK,
-                                 reinterpret_cast<const uint16_t *>(src8) + rkb * kBlockK, true, true,
-                                 p.hidden - rkb * kBlockK, lane);
+            if (G) {
+                ring.request(src0, count * p.block, lane);
+                src0 += count * p.block;
+            } else {
+                issue_block_bf16(ring.data + rstage * p.block, reinterpret_cast<const uint16_t *>(src0),
+                                 reinterpret_cast<const uint16_t *>(src8), true, true, p.hidden - rkb * kBlockK, lane);
+                src0 += kBlockK * 2;
+                src8 += kBlockK * 2;
+            }
             rkb += count;
             if (rkb == kb1) {
                 rkb = kb0;
@@ -218,52 +221,35 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) up_kernel(const Params
                 if (--rleft) aim();
             }
         }
-        if (!G) cp_async_commit();
+        if (!G) {
+            cp_async_commit();
+            rstage = rstage + 1 == STAGES ? 0 : rstage + 1;
+        }
     };
     const int slots = G ? p.slots_up : STAGES;
-    for (int s = 0; s < slots; ++s) request(s);
+    for (int s = 0; s < slots; ++s) request();
     cp_async_wait<G ? 0 : STAGES>();  // the rows
     __syncthreads();
 
     int stage = 0;
     for (; left; --left) {
         const int count = chunks.count[chunk];
-        const uint32_t xb = x0 + (g < count ? chunks.slot[chunk][g] / p.topk : p.m) * xs + 16 * t;
-        float C[1][4] = {}, sum[4] = {};
-        int next = kblocks * (slice + 1) / kSplit, quarter = slice;  // where the quarter ends
-        auto close = [&](int kb) {  // quarters that end at block kb join the sum
-            while (whole && kb == next && quarter < kSplit) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    sum[e] += C[0][e];
-                    C[0][e] = 0.0f;
-                }
-                ++quarter;
-                next = kblocks * (quarter + 1) / kSplit;
-            }
-        };
-        close(0);
+        const uint32_t xb[1] = {x0 + (g < count ? chunks.slot[chunk][g] / p.topk : p.m) * xs + 16 * t};
+        float S[1][4];
         if constexpr (G) {
-            for (int kb = kb0; kb < kb1; kb += p.per_up) {
-                const uint32_t at = ring.wait();
-                const int blocks = min(p.per_up, kb1 - kb);
-#pragma unroll 1
-                for (int b = 0; b < blocks; ++b) {
-                    const uint32_t x[1] = {xb + (kb + b) * (kBlockK * 2)};
-                    consume_block<G, false, 1>(at + b * p.block, p.fmt, x, C, lane);
-                    close(kb + b + 1);
-                }
-                ring.done();
-                request(0);
-            }
+            sum_quarters<G, false, 1>(ring, request, kblocks, kb0, kb1, p.per_up, p.block, p.fmt, xb, S, lane);
         } else {
-            for (int kb = kb0; kb < kb1; ++kb) {
-                cp_async_wait<STAGES - 1>();
-                const uint32_t x[1] = {xb + kb * (kBlockK * 2)};
-                consume_block_bf16<1>(ring.data + stage * p.block, x, C, lane);
-                close(kb + 1);
-                request(stage);
-                stage = stage + 1 == STAGES ? 0 : stage + 1;
+            for (int q = slice; q < (whole ? kSplit : slice + 1); ++q) {
+                float C[1][4] = {};
+                for (int kb = quarter_begin(kblocks, q); kb < quarter_begin(kblocks, q + 1); ++kb) {
+                    cp_async_wait<STAGES - 1>();
+                    const uint32_t x[1] = {xb[0] + kb * (kBlockK * 2)};
+                    consume_block_bf16<1>(ring.data + stage * p.block, x, C, lane);
+                    request();
+                    stage = stage + 1 == STAGES ? 0 : stage + 1;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[0][e] = q == slice ? C[0][e] : S[0][e] + C[0][e];
             }
         }
 #pragma unroll
@@ -271,8 +257,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) up_kernel(const Params
             if (2 * t + h < count) {
                 float *out = p.part + (int64_t)(chunks.slot[chunk][2 * t + h] * parts + slice) * 2 * p.inter +
                              tile * 8 + g;
-                out[0] = whole ? sum[h] : C[0][h];
-                out[p.inter] = whole ? sum[2 + h] : C[0][2 + h];
+                out[0] = S[0][h];
+                out[p.inter] = S[0][2 + h];
             }
         tile += step;
         while (tile >= tiles) {

@@ -8,11 +8,14 @@
 // unpacked to exact small integers (1.4 instructions a value) and multiplied
 // on the tensor core, 256 values x 8 rows an instruction.
 //
-// Work: a tile is 16 weight rows, one contiguous run of the packed weight.
-// KW = 4 warps (one worker) share a tile, each a contiguous quarter of its
-// blocks, and add their quarters in order through shared memory.  The split is
-// a function of k alone and a column of the matrix instruction never sees its
-// neighbours, so row i of the output has the same bits for every m.
+// Work: a tile is 16 weight rows, one contiguous run of the packed weight, and
+// its k is summed in quarters, added in order.  As many tiles as fill whole
+// rounds of all the grid's warps go one to a warp, which then never waits for
+// another; the rest, and all of a narrow weight's, go to four warps each, a
+// quarter to a warp, joined through shared memory (131072 x 2560, m = 4: 46.0 us
+// with every tile in quarters).  The quarters are a function of k alone and a
+// column of the matrix instruction never sees its neighbours, so row i of the
+// output has the same bits for every m.
 #include "w4_core.cuh"
 
 namespace mr {
@@ -77,7 +80,6 @@ __global__ void __launch_bounds__(256) pack_kernel(const uint8_t *__restrict__ q
 
 constexpr int kMaxRows = 16;
 constexpr int kMaxK = 1 << 20;               // far beyond what shared memory holds
-constexpr int kKW = 4;                       // warps that share a tile
 
 struct Params {
     const uint8_t *A;
@@ -99,7 +101,6 @@ __host__ __device__ constexpr int red_bytes(int warps, int NT) { return warps / 
 template <int G, bool F16, int NT, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) gemv_kernel(const Params p) {
     extern __shared__ __align__(128) uint8_t smem[];
-    constexpr int kWorkers = WARPS / kKW;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int worker = warp / kKW, slice = warp % kKW, g = lane >> 2, t = lane & 3;
     const int xs = (int)x_stride(p.kblocks), x_bytes = (p.m + 1) * xs;
@@ -110,19 +111,33 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) gemv_kernel(const Para
     grid_launch_dependents();
     ring.init(lane);
 
-    // This warp's blocks: its quarter [kb0, kb1) of tile first, first + step, ...
-    const int kb0 = p.kblocks * slice / kKW, kb1 = p.kblocks * (slice + 1) / kKW;
-    const int first = blockIdx.x * kWorkers + worker, step = gridDim.x * kWorkers;
-    int itile = kb0 < kb1 ? first : p.tiles, ikb = kb0;  // the next blocks to request
+    // Items: whole tiles [0, whole), then quarters of the others.  A warp takes
+    // item `first`, first + step, ...; step and `whole` are multiples of four,
+    // so the quarters of a tile are four neighbouring warps'.
+    const int first = blockIdx.x * WARPS + warp, step = gridDim.x * WARPS;
+    const int whole = p.tiles / step * step;
+    // The next request: `rleft` blocks from rsrc on, then item ritem.
+    const int64_t tile_bytes = (int64_t)p.kblocks * p.block;
+    const int qb = quarter_begin(p.kblocks, slice), qe = quarter_begin(p.kblocks, slice + 1);
+    int ritem = first, rleft = 0;
+    const uint8_t *rsrc = nullptr;
     auto request = [&]() {
-        if (itile >= p.tiles) return;
-        const int count = min(p.per, kb1 - ikb);
-        ring.request(p.W + ((int64_t)itile * p.kblocks + ikb) * p.block, count * p.block, lane);
-        ikb += count;
-        if (ikb == kb1) {
-            ikb = kb0;
-            itile += step;
+        while (rleft == 0) {
+            if (ritem < whole) {
+                rsrc = p.W + ritem * tile_bytes;
+                rleft = p.kblocks;
+            } else {
+                const int tile = whole + (ritem - whole) / kKW;
+                if (tile >= p.tiles) return;
+                rsrc = p.W + tile * tile_bytes + qb * p.block;
+                rleft = qe - qb;
+            }
+            ritem += step;
         }
+        const int count = min(p.per, rleft);
+        ring.request(rsrc, count * p.block, lane);
+        rsrc += count * p.block;
+        rleft -= count;
     };
     for (int s = 0; s < p.slots; ++s) request();
 
@@ -131,31 +146,35 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) gemv_kernel(const Para
     const int chunks = p.kblocks * (kBlockK / 8), live = p.k / 8;
     for (int r = warp; r <= p.m; r += WARPS)
         for (int c = lane; c < chunks; c += 32) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (r < p.m && c < live) v = *reinterpret_cast<const uint4 *>(p.A + r * p.lda + 16 * c);
-            *reinterpret_cast<uint4 *>(smem + r * xs + 16 * c) = v;
+            const bool in = r < p.m && c < live;
+            cp_async16_zfill(x0 + r * xs + 16 * c, in ? p.A + r * p.lda + 16 * c : p.A, in);
         }
+    cp_async_commit();
+    cp_async_wait<0>();
     __syncthreads();
 
     uint32_t xb[NT];
 #pragma unroll
     for (int c = 0; c < NT; ++c) xb[c] = x0 + min(8 * c + g, p.m) * xs + 16 * t;
-    int buf = 0;
-    for (int tile = first; tile < p.tiles; tile += step) {
-        float C[NT][4] = {};
-        for (int kb = kb0; kb < kb1; kb += p.per) {
-            const uint32_t at = ring.wait();
-            const int count = min(p.per, kb1 - kb);
-#pragma unroll 2
-            for (int b = 0; b < count; ++b) {
-                uint32_t x[NT];
+    auto store = [&](int tile, const float (&S)[NT][4]) {
 #pragma unroll
-                for (int c = 0; c < NT; ++c) x[c] = xb[c] + (kb + b) * (kBlockK * 2);
-                consume_block<G, F16, NT>(at + b * p.block, p.fmt, x, C, lane);
+        for (int c = 0; c < NT; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int col = 8 * c + 2 * t + (e & 1), row = tile * kTileRows + g + 8 * (e >> 1);
+                if (col < p.m && row < p.n) p.C[col * p.ldc + row] = S[c][e];
             }
-            ring.done();
-            request();
-        }
+    };
+    int item = first;
+    for (; item < whole; item += step) {
+        float S[NT][4];
+        sum_quarters<G, F16, NT>(ring, request, p.kblocks, 0, p.kblocks, p.per, p.block, p.fmt, xb, S, lane);
+        store(item, S);
+    }
+    int buf = 0;
+    for (int tile; (tile = whole + (item - whole) / kKW) < p.tiles; item += step) {
+        float S[NT][4];
+        sum_quarters<G, F16, NT>(ring, request, p.kblocks, qb, qe, p.per, p.block, p.fmt, xb, S, lane);
         // The first warp adds the quarters in order.  Two buffers: a warp
         // writes one again only after the barrier of the tile between, which
         // the first warp reaches after reading it.
@@ -164,7 +183,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) gemv_kernel(const Para
 #pragma unroll
             for (int c = 0; c < NT; ++c)
                 asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(part + ((slice - 1) * NT + c) * 512),
-                             "f"(C[c][0]), "f"(C[c][1]), "f"(C[c][2]), "f"(C[c][3])
+                             "f"(S[c][0]), "f"(S[c][1]), "f"(S[c][2]), "f"(S[c][3])
                              : "memory");
         }
         asm volatile("bar.sync %0, %1;" ::"r"(1 + worker), "n"(kKW * 32) : "memory");
@@ -174,18 +193,12 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) gemv_kernel(const Para
 #pragma unroll
                 for (int c = 0; c < NT; ++c) {
                     const uint4 v = lds128(part + (s * NT + c) * 512);
-                    C[c][0] += __uint_as_float(v.x);
-                    C[c][1] += __uint_as_float(v.y);
-                    C[c][2] += __uint_as_float(v.z);
-                    C[c][3] += __uint_as_float(v.w);
+                    S[c][0] += __uint_as_float(v.x);
+                    S[c][1] += __uint_as_float(v.y);
+                    S[c][2] += __uint_as_float(v.z);
+                    S[c][3] += __uint_as_float(v.w);
                 }
-#pragma unroll
-            for (int c = 0; c < NT; ++c)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int col = 8 * c + 2 * t + (e & 1), row = tile * kTileRows + g + 8 * (e >> 1);
-                    if (col < p.m && row < p.n) p.C[col * p.ldc + row] = C[c][e];
-                }
+            store(tile, S);
         }
         buf ^= 1;
     }

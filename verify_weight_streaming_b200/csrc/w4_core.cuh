@@ -316,6 +316,55 @@ struct Ring {
     }
 };
 
+// ---- quarters of k ---------------------------------------------------------
+
+// k is summed in kKW = 4 quarters of its blocks, added in order: the split that
+// lets four warps share a tile, kept by a warp that has a tile to itself, so
+// that an output's bits do not depend on which of the two it was.
+constexpr int kKW = 4;
+__device__ __forceinline__ int quarter_begin(int kblocks, int q) { return kblocks * q / kKW; }
+
+// S = the quarters of blocks [begin, end) of a tile, in order; `request` asks
+// for the blocks that follow, a stage at a time.
+template <int G, bool F16, int NT, class Request>
+__device__ __forceinline__ void sum_quarters(Ring &ring, Request &request, int kblocks, int begin, int end, int per,
+                                             int block, uint32_t fmt, const uint32_t (&xb)[NT], float (&S)[NT][4],
+                                             int lane) {
+    float C[NT][4] = {};
+#pragma unroll
+    for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[c][e] = 0.0f;
+    int q = 0, close = 0;  // the quarter's end
+    auto next = [&](int kb) {
+        while (close <= kb && q < kKW) close = quarter_begin(kblocks, ++q);
+    };
+    next(begin);
+    for (int kb = begin; kb < end; kb += per) {
+        uint32_t at = ring.wait();
+        const int stop = min(kb + per, end);
+#pragma unroll 1
+        for (int b = kb; b < stop; ++b, at += block) {
+            uint32_t x[NT];
+#pragma unroll
+            for (int c = 0; c < NT; ++c) x[c] = xb[c] + b * (kBlockK * 2);
+            consume_block<G, F16, NT>(at, fmt, x, C, lane);
+            if (b + 1 == close) {
+#pragma unroll
+                for (int c = 0; c < NT; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        S[c][e] += C[c][e];
+                        C[c][e] = 0.0f;
+                    }
+                next(b + 1);
+            }
+        }
+        ring.done();
+        request();
+    }
+}
+
 // Allow `kernel` all the shared memory the device offers, once per device.
 template <class K>
 bool allow_smem(K kernel, std::atomic<uint64_t> &done) {
