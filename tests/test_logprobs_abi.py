@@ -29,7 +29,6 @@ def call(x=A, ld=100, dt=mr.MR_F32, m=2, n=100, scale=1.0, tok=A, ldt=3, ntok=3,
     (dict(ent=ODD), mr.MR_ERR_MISALIGNED), (dict(idx=ODD), mr.MR_ERR_MISALIGNED), (dict(tlp=ODD), mr.MR_ERR_MISALIGNED),
     (dict(topk=33, ldo=33), mr.MR_ERR_UNSUPPORTED), (dict(ntok=257, ldt=257, ldp=257), mr.MR_ERR_UNSUPPORTED),
     (dict(n=2 ** 30 + 1, ld=2 ** 31), mr.MR_ERR_UNSUPPORTED),
-    (dict(m=2 ** 31 - 1, n=10 ** 6, ld=10 ** 6), mr.MR_ERR_UNSUPPORTED),
 ])
 def test_refusals(kw, code):
     assert call(**kw) == code

@@ -138,10 +138,10 @@ def _current_stream_handle() -> int:
 
 def _stream(stream):
     if stream is None:
-        return ctypes.c_void_p(_current_stream_handle())
+        return _current_stream_handle()
     if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
 def _rows(t, name):
@@ -152,10 +152,15 @@ def _rows(t, name):
     return sh[0], sh[1], st[0]
 
 
+_dtype_codes: dict = {}
+
+
 def _dtype_code(t) -> int:
-    import torch
-    return {torch.float16: MR_F16, torch.bfloat16: MR_BF16, torch.float32: MR_F32,
-            torch.int16: MR_BF16}.get(t.dtype, -1)
+    if not _dtype_codes:
+        import torch
+        _dtype_codes.update({torch.float16: MR_F16, torch.bfloat16: MR_BF16, torch.float32: MR_F32,
+                             torch.int16: MR_BF16})
+    return _dtype_codes.get(t.dtype, -1)
 
 
 def mrgemv_bf16(A, Wt, C, stream=None, flags: int = 0) -> None:
@@ -445,35 +450,43 @@ def token_logprobs(logits, tokens=None, logprob=None, scale: float = 1.0, lse=No
     """Log probabilities (fp32) of logits[m,n] (fp32, bf16 or f16) times ``scale``, into whichever outputs are given:
     logprob[m,t] of tokens[m,t] (int32), lse[m], entropy[m], and the top_idx.shape[1] best alternatives
     top_idx[m,k] (int32), top_logprob[m,k]."""
-    import torch
     m, n, ldl = _rows(logits, "logits")
-    dtype = -1 if logits.dtype == torch.int16 else _dtype_code(logits)
-    tptr = lptr = iptr = vptr = None
+    dtype = _dtype_code(logits)
+    if dtype == MR_BF16 and not logits.is_floating_point():  # no raw bit patterns here
+        dtype = -1
+    tptr = lptr = iptr = vptr = sptr = eptr = None
     ntok = ldt = ldp = topk = ldo = 0
     if (tokens is None) != (logprob is None):
         raise ValueError("tokens and logprob go together")
     if tokens is not None:
-        if tokens.dim() != 2 or tokens.shape[0] != m or logprob.shape != tokens.shape:
+        shape = tokens.shape
+        if len(shape) != 2 or shape[0] != m or logprob.shape != shape:
             raise ValueError("tokens and logprob must be [m, t]")
-        if tokens.shape[1]:
+        if shape[1]:
             _, ntok, ldt = _rows(tokens, "tokens")
             ldp = _rows(logprob, "logprob")[2]
             tptr, lptr = tokens.data_ptr(), logprob.data_ptr()
-    for t, name in ((lse, "lse"), (entropy, "entropy")):
-        if t is not None and (t.dim() != 1 or t.shape[0] != m or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous [m] tensor")
-    if top_idx is None and top_logprob is not None:
-        raise ValueError("top_logprob needs top_idx")
-    if top_idx is not None:
-        if top_idx.dim() != 2 or top_idx.shape[0] != m:
+    if lse is not None:
+        if lse.shape != (m,) or lse.stride(0) != 1:
+            raise ValueError("lse must be a contiguous [m] tensor")
+        sptr = lse.data_ptr()
+    if entropy is not None:
+        if entropy.shape != (m,) or entropy.stride(0) != 1:
+            raise ValueError("entropy must be a contiguous [m] tensor")
+        eptr = entropy.data_ptr()
+    if top_idx is None:
+        if top_logprob is not None:
+            raise ValueError("top_logprob needs top_idx")
+    else:
+        shape = top_idx.shape
+        if len(shape) != 2 or shape[0] != m:
             raise ValueError("top_idx must be [m, k]")
-        if top_logprob is not None and (top_logprob.shape != top_idx.shape or top_logprob.stride() != top_idx.stride()):
+        if top_logprob is not None and (top_logprob.shape != shape or top_logprob.stride() != top_idx.stride()):
             raise ValueError("top_logprob must match top_idx's shape and stride")
-        if top_idx.shape[1]:
+        if shape[1]:
             _, topk, ldo = _rows(top_idx, "top_idx")
             iptr = top_idx.data_ptr()
             vptr = None if top_logprob is None else top_logprob.data_ptr()
-    st = lib.token_logprobs(logits.data_ptr(), ldl, dtype, m, n, scale, tptr, ldt, ntok, lptr, ldp,
-                            None if lse is None else lse.data_ptr(), None if entropy is None else entropy.data_ptr(),
-                            topk, iptr, vptr, ldo, _stream(stream))
+    st = lib.token_logprobs(logits.data_ptr(), ldl, dtype, m, n, scale, tptr, ldt, ntok, lptr, ldp, sptr, eptr, topk,
+                            iptr, vptr, ldo, _stream(stream))
     _check(st, "token_logprobs")

@@ -21,8 +21,9 @@
 //    (Added up instead by the warp that stores a tile's last share, it took
 //    323 us in place of 234 at 16 rows: a few warps get most of that work.)
 //
-// The three overlap by programmatic launch: down requests its first weights
-// and combine computes its softmax before the kernel ahead has finished.
+// The three are launched programmatically: as a kernel's CTAs leave, the next
+// one's build their lists and request their first weights (down) or compute the
+// softmax (combine) before the rest has finished.
 // The split of k depends on the sizes of the expert alone and sums run in a
 // fixed order, so a row's bits depend on its own x, ids and weights only.
 #include "w4_core.cuh"
@@ -61,75 +62,105 @@ struct Params {
     uint32_t fmt;
 };
 
-// The chunks of a call: up to `cap` choices (slots t * topk + s) of one expert.
+// The chunks of a call: up to `cap` choices (slots t * topk + s) of one expert,
+// in the order of their first slots.
+constexpr int kTable = 1024;
 struct alignas(16) Chunks {
     int32_t ids[kMaxSlots];
-    uint32_t lead[kMaxSlots / 32];
     int32_t expert[kMaxSlots];
     int32_t count[kMaxSlots];
-    uint16_t slot[kMaxSlots][kChunk];
+    uint32_t lead[kMaxSlots / 32];      // slots that open a chunk
+    union {
+        uint16_t slot[kMaxSlots][kChunk];
+        struct {                        // while it is built, by expert
+            int first[kTable], seen[kTable];
+        } table;
+    };
     int n;
 };
 constexpr int kChunkBytes = (sizeof(Chunks) + 127) / 128 * 128;  // at the start of dynamic shared memory
 
-// Built by every thread of the CTA; deterministic (chunks in the order of
-// their first slot).
-template <int kThreads>
-__device__ void build_chunks(Chunks &c, const Params &p) {
-    const int S = p.m * p.topk, lane = threadIdx.x & 31;
-    for (int s = threadIdx.x; s < kMaxSlots; s += kThreads) {
-        if (s >= S) {
-            c.ids[s] = -1;
-            continue;
-        }
-        // from L2: the producer of ids may have run while this grid was starting
-        const int64_t e = (int64_t)__ldcg(p.ids + (s / p.topk) * p.ldr + s % p.topk);
-        c.ids[s] = (e >= p.base && e - p.base < p.experts) ? (int32_t)(e - p.base) : -1;
-        c.count[s] = 0;
-    }
-    __syncthreads();
-    int rank[kMaxSlots / kThreads], lead[kMaxSlots / kThreads];
+// A thread's slots' experts, -1 where there is none held here: loaded ahead of
+// build_chunks, from L2 (the producer of ids may have run while this grid was
+// starting).
+template <int WARPS>
+struct Choices {
+    static constexpr int N = kMaxSlots / (WARPS * 32);
+    int e[N];
+    __device__ __forceinline__ explicit Choices(const Params &p) {
 #pragma unroll
-    for (int i = 0; i < kMaxSlots / kThreads; ++i) {
-        const int s = i * kThreads + threadIdx.x;
-        const int e = s < S ? c.ids[s] : -1;
-        int n = 0, first = s;
-        if (e >= 0) {
-            int of = 0;  // n % cap
-            for (int q = 0; q < s; q += 4) {
-                const int4 v = *reinterpret_cast<const int4 *>(c.ids + q);
-                const int four[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (four[j] == e && q + j < s) {
-                        if (of == 0) first = q + j;
-                        of = of + 1 == p.cap ? 0 : of + 1;
-                        ++n;
-                    }
+        for (int i = 0; i < N; ++i) {
+            const int s = i * WARPS * 32 + threadIdx.x;
+            e[i] = -1;
+            if (s < p.m * p.topk) {
+                const int64_t id = (int64_t)__ldcg(p.ids + (s / p.topk) * p.ldr + s % p.topk);
+                if (id >= p.base && id - p.base < p.experts) e[i] = (int)(id - p.base);
             }
-            if (of == 0) first = s;
         }
-        rank[i] = n;
-        lead[i] = first;
-        const uint32_t bits = __ballot_sync(0xffffffffu, e >= 0 && first == s);
-        if (lane == 0) c.lead[s / 32] = bits;
     }
-    __syncthreads();
+};
+
+// Built by every thread of the CTA, the same in every CTA.  With a table entry
+// an expert, an atomic minimum finds its first slot and an atomic count the
+// slots' places (in any order: a place changes no result).  Where there are more
+// experts than entries, or one has choices for several chunks (whose members
+// must be the same in every CTA), places come from a scan of the slots before.
+template <int WARPS>
+__device__ void build_chunks(Chunks &c, const Params &p, const Choices<WARPS> &mine) {
+    constexpr int N = Choices<WARPS>::N, kThreads = WARPS * 32;
+    const int S = p.m * p.topk, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < kTable; i += kThreads) {
+        c.table.first[i] = kMaxSlots;
+        c.table.seen[i] = 0;
+    }
 #pragma unroll
-    for (int i = 0; i < kMaxSlots / kThreads; ++i) {
-        const int s = i * kThreads + threadIdx.x;
-        const int e = s < S ? c.ids[s] : -1;
-        if (e < 0) continue;
-        int chunk = __popc(c.lead[lead[i] / 32] & ((1u << (lead[i] & 31)) - 1u));
-        for (int w = 0; w < lead[i] / 32; ++w) chunk += __popc(c.lead[w]);
-        c.slot[chunk][rank[i] % p.cap] = (uint16_t)s;
-        atomicAdd(&c.count[chunk], 1);
-        if (lead[i] == s) c.expert[chunk] = e;
+    for (int i = 0; i < N; ++i) c.count[i * kThreads + threadIdx.x] = 0;
+    __syncthreads();
+    int place[N], first[N];
+    bool scan = p.experts > kTable;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int s = i * kThreads + threadIdx.x, e = mine.e[i];
+        c.ids[s] = e;
+        if (e >= 0 && p.experts <= kTable) {
+            atomicMin(&c.table.first[e], s);
+            place[i] = atomicAdd(&c.table.seen[e], 1);
+            scan = scan || place[i] >= p.cap;
+        }
     }
-    if (threadIdx.x == 0) {
-        int n = 0;
-        for (int w = 0; w < kMaxSlots / 32; ++w) n += __popc(c.lead[w]);
-        c.n = n;
+    scan = __syncthreads_or(scan);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int s = i * kThreads + threadIdx.x, e = mine.e[i];
+        if (!scan) {
+            first[i] = e >= 0 ? c.table.first[e] : -1;
+        } else {
+            place[i] = 0;
+            first[i] = e >= 0 ? s : -1;
+            for (int q = 0; e >= 0 && q < s; ++q)
+                if (c.ids[q] == e) {
+                    if (place[i] == 0) first[i] = q;
+                    place[i] = place[i] + 1 == p.cap ? 0 : place[i] + 1;
+                }
+            if (place[i] == 0 && e >= 0) first[i] = s;
+        }
+        const uint32_t leads = __ballot_sync(0xffffffffu, first[i] == s);
+        if (lane == 0) c.lead[s / 32] = leads;
+    }
+    __syncthreads();  // the table has been read
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int s = i * kThreads + threadIdx.x;
+        if (first[i] < 0) continue;
+        int chunk = __popc(c.lead[first[i] / 32] & ((1u << (first[i] & 31)) - 1u));
+        for (int w = 0; w < first[i] / 32; ++w) chunk += __popc(c.lead[w]);
+        c.slot[chunk][place[i]] = (uint16_t)s;
+        atomicAdd(&c.count[chunk], 1);
+        if (first[i] == s) c.expert[chunk] = mine.e[i];
+    }
+    if (threadIdx.x < 32) {
+        const int n = __reduce_add_sync(0xffffffffu, lane < (S + 31) / 32 ? __popc(c.lead[lane]) : 0);
+        if (lane == 0) c.n = n;
     }
     __syncthreads();
 }
@@ -141,8 +172,10 @@ __host__ __device__ inline int row_stride(int k) { return (k + kBlockK - 1) / kB
 // lane copies the bytes it reads itself.
 
 // Whether a warp of the up kernel sums all quarters of a tile itself: when
-// that still gives every warp two tiles.
-__device__ __forceinline__ bool whole_tiles(const Params &p, int chunks) {
+// that still gives every warp two tiles.  (The down projection has no quarters:
+// with its shorter k they cost more in partial sums than they balanced, one bf16
+// row 29.8 us without, 31.3 with.)
+__device__ __forceinline__ bool whole_up(const Params &p, int chunks) {
     return chunks * (p.inter / 8) >= 2 * p.up_warps;
 }
 
@@ -163,6 +196,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) up_kernel(const Params
     if (G) ring.init(lane);
     grid_dependency_wait();
     grid_launch_dependents();  // after the wait: the next grid may read ids at once
+    const Choices<WARPS> choices(p);
     // The rows, and one of zeros, on their way while the chunks are built.
     const int pieces = kblocks * (kBlockK / 8), live = p.hidden / 8;
     for (int r = warp; r <= p.m; r += WARPS)
@@ -171,11 +205,11 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) up_kernel(const Params
             cp_async16_zfill(x0 + r * xs + 16 * c, in ? p.X + r * p.ldx + 16 * c : p.X, in);
         }
     cp_async_commit();
-    build_chunks<WARPS * 32>(chunks, p);
+    build_chunks<WARPS>(chunks, p, choices);
 
     // This CTA's run of items (tiles, or quarters of them), a warp every
     // WARPS-th: a warp of quarters always has the same one.
-    const bool whole = whole_tiles(p, chunks.n);
+    const bool whole = whole_up(p, chunks.n);
     const int shift = whole ? 0 : 2, parts = whole ? 1 : kSplit;
     const int64_t items = (int64_t)(chunks.n * tiles) << shift;
     const int i0 = (int)(items * blockIdx.x / gridDim.x) + warp, i1 = (int)(items * (blockIdx.x + 1) / gridDim.x);
@@ -274,39 +308,48 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) up_kernel(const Params
 template <int THREADS>
 __device__ void stage_activations(uint8_t *smem, const Params &p, const Chunks &c, int chunk, int parts, int hs,
                                   int width) {
-    for (int i = 0; i < c.count[chunk]; ++i) {
-        const float *q0 = p.part + (int64_t)c.slot[chunk][i] * parts * 2 * p.inter;
-        for (int j = threadIdx.x; j < width; j += THREADS) {
-            float h = 0.0f;
-            if (j < p.inter) {
-                const float *q = q0 + j;
-                float gate = q[0], up = q[p.inter];
-                if (parts > 1) {
-                    float v[2 * (kSplit - 1)];
+    // four columns a thread: all of its loads are in flight together
+    const int quads = width / 4;
+    for (int e = threadIdx.x; e < c.count[chunk] * quads; e += THREADS) {
+        const int i = e / quads, j = 4 * (e % quads);
+        float gate[4] = {}, up[4] = {};
+        if (j < p.inter) {
+            const float *q = p.part + (int64_t)c.slot[chunk][i] * parts * 2 * p.inter + j;
+            float4 v[2 * kSplit];
 #pragma unroll
-                    for (int s = 0; s < kSplit - 1; ++s) {
-                        v[2 * s] = q[(2 * s + 2) * p.inter];
-                        v[2 * s + 1] = q[(2 * s + 3) * p.inter];
-                    }
+            for (int s = 0; s < kSplit; ++s)
+                if (s < parts) {
+                    v[2 * s] = *reinterpret_cast<const float4 *>(q + 2 * s * p.inter);
+                    v[2 * s + 1] = *reinterpret_cast<const float4 *>(q + (2 * s + 1) * p.inter);
+                }
 #pragma unroll
-                    for (int s = 0; s < kSplit - 1; ++s) {
-                        gate += v[2 * s];
-                        up += v[2 * s + 1];
+            for (int s = 0; s < kSplit; ++s)
+                if (s < parts) {
+                    const float a[4] = {v[2 * s].x, v[2 * s].y, v[2 * s].z, v[2 * s].w};
+                    const float b[4] = {v[2 * s + 1].x, v[2 * s + 1].y, v[2 * s + 1].z, v[2 * s + 1].w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        gate[x] += a[x];
+                        up[x] += b[x];
                     }
                 }
-                h = gate / (1.0f + expf(-gate)) * up;
-            }
-            // h = hi + mid + lo exactly: each piece takes the next 8 bits
-            const uint32_t hi = __float_as_uint(h) & 0xFFFF0000u;
-            const bool finite = (hi & 0x7F800000u) != 0x7F800000u;
-            const float r = finite ? h - __uint_as_float(hi) : 0.0f;
-            const uint32_t mid = __float_as_uint(r) & 0xFFFF0000u;
-            const uint32_t lo = __float_as_uint(r - __uint_as_float(mid));
-            uint8_t *row = smem + (3 * i) * hs + 2 * j;
-            *reinterpret_cast<uint16_t *>(row) = (uint16_t)(hi >> 16);
-            *reinterpret_cast<uint16_t *>(row + hs) = (uint16_t)(mid >> 16);
-            *reinterpret_cast<uint16_t *>(row + 2 * hs) = (uint16_t)(lo >> 16);
         }
+        // h = hi + mid + lo exactly: each piece takes the next 8 bits
+        uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const float h = gate[x] / (1.0f + expf(-gate[x])) * up[x];
+            hi[x] = __float_as_uint(h) & 0xFFFF0000u;
+            const bool finite = (hi[x] & 0x7F800000u) != 0x7F800000u;
+            const float r = finite ? h - __uint_as_float(hi[x]) : 0.0f;
+            mid[x] = __float_as_uint(r) & 0xFFFF0000u;
+            lo[x] = __float_as_uint(r - __uint_as_float(mid[x]));
+        }
+        uint8_t *row = smem + (3 * i) * hs + 2 * j;
+        *reinterpret_cast<uint2 *>(row) = make_uint2(hi[0] >> 16 | hi[1], hi[2] >> 16 | hi[3]);
+        *reinterpret_cast<uint2 *>(row + hs) = make_uint2(mid[0] >> 16 | mid[1], mid[2] >> 16 | mid[3]);
+        *reinterpret_cast<uint2 *>(row + 2 * hs) =
+            make_uint2(lo[0] >> 16 | (lo[1] & 0xFFFF0000u), lo[2] >> 16 | (lo[3] & 0xFFFF0000u));
     }
 }
 
@@ -323,8 +366,9 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) down_kernel(const Para
     Ring ring(ring0 + warp * ring_bytes, ring0 + WARPS * ring_bytes + warp * p.slots_down * 8, p.slots_down,
               p.per_down * p.block);
     grid_launch_dependents();
+    const Choices<WARPS> choices(p);
     if (G) ring.init(lane);
-    build_chunks<WARPS * 32>(chunks, p);
+    build_chunks<WARPS>(chunks, p, choices);
 
     const int64_t units = (int64_t)chunks.n * tiles;
     const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
@@ -374,7 +418,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) down_kernel(const Para
 
     grid_dependency_wait();  // the up projection's partial sums
     if (u0 >= u1) return;
-    const int parts = whole_tiles(p, chunks.n) ? 1 : kSplit;
+    const int parts = whole_up(p, chunks.n) ? 1 : kSplit;
     int stage = 0;
     // The address of a lane's column of column tile c: piece g % 4 of choice
     // 2c + g / 4, zeros for the fourth and for choices that are not there.
@@ -484,13 +528,13 @@ __global__ void __launch_bounds__(128) combine_kernel(const Params p) {
     const int j = blockIdx.x * blockDim.x + threadIdx.x;
     if (j >= p.hidden) return;
     float y = 0.0f;
-    for (int s0 = 0; s0 < p.topk; s0 += 8) {
-        float v[8];
+    for (int s0 = 0; s0 < p.topk; s0 += 16) {
+        float v[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 16; ++i)
             v[i] = s0 + i < p.topk && held[s0 + i] ? p.down[(int64_t)(row * p.topk + s0 + i) * p.hidden + j] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 16; ++i)
             if (s0 + i < p.topk && held[s0 + i]) y = fmaf(w[s0 + i], v[i], y);
     }
     if (p.out_bf16)
@@ -515,42 +559,48 @@ cudaError_t launch_one(K kernel, dim3 grid, int threads, size_t smem, cudaStream
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// Warps of a CTA and its shared memory.  Two CTAs of 8 warps share an SM where
-// the activations leave each 40 KB of ring; otherwise one CTA of 16 warps, or
-// of 8 where a bf16 ring (4 KB a block) leaves no room for 16.
+// Warps of a CTA, its CTAs to an SM and its shared memory.
 struct Plan {
-    int warps = 0, stages = 0;
+    int warps = 0, per_sm = 0, stages = 0;
     size_t smem = 0;
 };
 
-Plan plan(size_t optin, size_t fixed, int length, int block, bool packed, int &per, int &slots) {
+// A plan of `per_sm` CTAs of `warps` within `limit` bytes each; `length`:
+// consecutive blocks a warp can use (packed blocks), `stages`: blocks in flight
+// (bf16).
+Plan fit(size_t limit, int per_sm, int warps, int stages, size_t fixed, int length, int block, bool packed, int &per,
+         int &slots) {
     Plan out;
-    const size_t half = (optin + 1024) / 2 - 1024;
-    auto fits = [&](int warps, size_t limit, size_t ring) {
-        return fixed + 32 * warps + ring <= limit;
-    };
-    if (packed) {
-        out.warps = fits(8, half, 40 * 1024) ? 8 : 16;
-        const size_t limit = out.warps == 8 ? half : optin;
-        if (!fits(out.warps, limit, (size_t)2 * out.warps * block)) return Plan();
-        const int blocks = (int)((limit - fixed - 32 * out.warps) / out.warps / block);
-        per = std::min(length, blocks / 2);
-        slots = std::min(4, blocks / per);
-        out.smem = fixed + 32 * out.warps + (size_t)out.warps * slots * per * block;
-        return out;
-    }
-    per = 1;
-    const int tries[4][3] = {{8, 2, 0}, {16, 2, 1}, {8, 3, 1}, {8, 2, 1}};  // warps, stages, whole SM
-    for (const auto &c : tries)
-        if (fits(c[0], c[2] ? optin : half, (size_t)c[0] * c[1] * block)) {
-            out.warps = c[0];
-            out.stages = slots = c[1];
-            out.smem = fixed + 32 * c[0] + (size_t)c[0] * c[1] * block;
-            return out;
-        }
+    fixed += 32 * warps;  // barriers
+    const int blocks = limit > fixed ? (int)((limit - fixed) / warps / block) : 0;
+    if (blocks < (packed ? 2 : stages)) return out;
+    per = packed ? std::min(length, blocks / 2) : 1;
+    slots = packed ? std::min(4, blocks / per) : stages;
+    out.warps = warps;
+    out.per_sm = per_sm;
+    out.stages = stages;
+    out.smem = fixed + (size_t)warps * slots * per * block;
     return out;
 }
 
+// Two CTAs of 8 warps share an SM where the activations leave each a ring (40 KB
+// of packed blocks, two bf16 blocks a warp); otherwise one CTA of 16 warps, or for
+// bf16 of 8 with a deeper ring.  (One CTA of 8 of each kernel sharing an SM, so
+// that the down projection stands ready when the up projection ends, was
+// slower: one bf16 row 28.4 us against 26.8, 8 rows of 4-bit experts 71 against 57.)
+Plan plan(size_t optin, size_t fixed, int length, int block, bool packed, int &per, int &slots) {
+    const size_t half = (optin + 1024) / 2 - 1024;
+    Plan out;
+    if (packed) {
+        if (fixed + 40 * 1024 < half) out = fit(half, 2, 8, 0, fixed, length, block, true, per, slots);
+        if (!out.warps) out = fit(optin, 1, 16, 0, fixed, length, block, true, per, slots);
+        return out;
+    }
+    const int tries[4][2] = {{8, 2}, {16, 2}, {8, 3}, {8, 2}};  // warps, stages; the first in half an SM
+    for (int i = 0; i < 4 && !out.warps; ++i)
+        out = fit(i ? optin : half, i ? 1 : 2, tries[i][0], tries[i][1], fixed, 1, block, false, per, slots);
+    return out;
+}
 Plan up_plan(Params &p, size_t optin) {
     const int kblocks = (p.hidden + kBlockK - 1) / kBlockK;
     return plan(optin, kChunkBytes + (size_t)(p.m + 1) * row_stride(p.hidden), (kblocks + kSplit - 1) / kSplit,
@@ -558,14 +608,11 @@ Plan up_plan(Params &p, size_t optin) {
 }
 Plan down_plan(Params &p, size_t optin) {
     const int kblocks = (p.inter + kBlockK - 1) / kBlockK;
-    return plan(optin, kChunkBytes + (size_t)(3 * p.cap + 1) * row_stride(p.inter), kblocks, p.block,
-                p.fmt != 0, p.per_down, p.slots_down);
+    return plan(optin, kChunkBytes + (size_t)(3 * p.cap + 1) * row_stride(p.inter), kblocks, p.block, p.fmt != 0,
+                p.per_down, p.slots_down);
 }
 
-dim3 grid_of(const Plan &pl) {
-    const bool two = pl.warps == 8 && 2 * (pl.smem + 1024) <= (size_t)mr_host::max_smem_optin() + 1024;
-    return dim3((unsigned)(mr_host::sm_count() * (two ? 2 : 1)));
-}
+dim3 grid_of(const Plan &pl) { return dim3((unsigned)(mr_host::sm_count() * pl.per_sm)); }
 
 template <int G, int WARPS, int STAGES>
 cudaError_t launch_up(const Params &p, const Plan &pl, cudaStream_t stream) {

@@ -687,7 +687,6 @@ extern "C" mr_status token_logprobs(const void *logits, int64_t ldl, int32_t dty
     const int64_t most = (int64_t)mr_host::sm_count() * (topk ? 7 : 9) / 2;
     p.cluster = 1;
     while (p.cluster < p.pieces && (int64_t)m * p.cluster * 2 <= most) p.cluster *= 2;
-    if ((int64_t)m * p.cluster > (int64_t)INT32_MAX) return MR_ERR_UNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (dtype) {
         case MR_F32: return mr::logprobs::launch<MR_F32>(p, m, s);
