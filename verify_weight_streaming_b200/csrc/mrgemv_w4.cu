@@ -206,8 +206,11 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) gemv_kernel(const Para
 
 // Shared memory and the launch's shape.  Two CTAs of 8 warps share an SM when
 // the activations leave each of them 40 KB of ring (the next launch's CTA then
-// also finds room under programmatic launch); otherwise one of 16 warps.  A
-// stage holds a warp's whole quarter of a tile where two of them fit.
+// also finds room under programmatic launch); otherwise, or where every warp gets
+// two tiles or more, one of 16 warps, whose rings are longer as the activations
+// are there once (131072 x 2560, m = 4: 42.2 and 40.3 us).  A stage holds a warp's
+// whole quarter of a tile where two of them fit (five blocks a stage there; with
+// three 42.8 us, with two 45.1).
 struct Plan {
     int warps = 0;
     size_t smem = 0;
@@ -216,7 +219,9 @@ struct Plan {
 Plan plan(Params &p, size_t optin) {
     Plan out;
     const int NT = p.m > 8 ? 2 : 1, quarter = (p.kblocks + kKW - 1) / kKW;
+    const bool deep = p.tiles >= 2 * 16 * mr_host::sm_count();
     for (int warps : {8, 16}) {
+        if (warps == 8 && deep) continue;
         const size_t limit = warps == 8 ? (optin + 1024) / 2 - 1024 : optin;
         const size_t fixed = (size_t)(p.m + 1) * x_stride(p.kblocks) + red_bytes(warps, NT) + 8 * 4 * warps;
         if (fixed + (warps == 8 ? 40 * 1024 : 2 * warps * p.block) > limit) continue;
