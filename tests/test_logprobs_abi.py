@@ -52,5 +52,7 @@ def test_binding_refusals():
                 dict(top_logprob=tlp), dict(top_idx=idx[:1]), dict(top_idx=idx, top_logprob=tlp[:, :3])):
         with pytest.raises(ValueError):
             mr.token_logprobs(x, **bad)
-    with pytest.raises(mr.MrError):
-        mr.token_logprobs(x.to(torch.int16), lse=torch.zeros(2), stream=0)
+    for bad in (dict(tokens=tok.long(), logprob=lp), dict(tokens=tok, logprob=lp.double()), dict(lse=torch.zeros(2).half()),
+                dict(top_idx=idx.long()), dict(lse=torch.zeros(2))):  # the last: not on a CUDA device
+        with pytest.raises(ValueError):
+            mr.token_logprobs(x, **bad)

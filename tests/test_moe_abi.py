@@ -90,6 +90,8 @@ def test_binding_refusals():
     for bad in (dict(ids=torch.zeros(3, 4, dtype=torch.int32)), dict(weights=torch.zeros(2, 5)),
                 dict(weights=torch.zeros(4, 2).t()), dict(Y=torch.zeros(2, 120)), dict(Wup=torch.zeros(8, 64, 128, dtype=bf)),
                 dict(Wdown=torch.zeros(8, 64, 64, dtype=bf)), dict(Wup=torch.zeros(8, 128, dtype=bf)),
-                dict(Wdown=torch.zeros(8, 64, 128, dtype=bf).transpose(1, 2))):
+                dict(Wdown=torch.zeros(8, 64, 128, dtype=bf).transpose(1, 2)), dict(X=torch.zeros(2, 128)),
+                dict(ids=torch.zeros(2, 4, dtype=torch.int64)), dict(weights=torch.zeros(2, 4, dtype=bf)),
+                dict(Wup=torch.zeros(8, 128, 128)), dict()):  # the last: not on a CUDA device
         with pytest.raises(ValueError):
             mr.moe_window_bf16(**dict(good, **bad))

@@ -85,3 +85,10 @@ def test_binding_refusals():
             mr.w4_pack(args["q"], args["s"], args["z"], args["out"])
     with pytest.raises(ValueError):
         mr.mrgemv_w4(torch.zeros((2, 128), dtype=torch.bfloat16), out, torch.zeros((3, 16)), 128)
+    a = torch.zeros((2, 128), dtype=torch.bfloat16)
+    for c, packed in ((torch.zeros((2, 16)).half(), out), (torch.zeros((2, 16)), out.to(torch.int32)),
+                      (torch.zeros((2, 16)), out)):  # the last: not on a CUDA device
+        with pytest.raises(ValueError):
+            mr.mrgemv_w4(a, packed, c, 128)
+    with pytest.raises(ValueError):
+        mr.w4_pack(q, s, None, out)

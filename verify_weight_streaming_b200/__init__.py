@@ -354,9 +354,33 @@ def mr_selftest_wait_timeout(limit_us: int, stream=None) -> None:
     _check(lib.mr_selftest_wait_timeout(limit_us, _stream(stream)), "mr_selftest_wait_timeout")
 
 
+_torch = None
+
+
+def _types():
+    """torch, imported on the first call that needs its dtypes."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _here(*tensors) -> None:
+    """Refuses tensors that are not on the current CUDA device (None is skipped): the kernels run there."""
+    want = None
+    for t in tensors:
+        if t is not None:
+            have = t.get_device()
+            if want is None and have >= 0:
+                want = _types()._C._cuda_getDevice()
+            if have != want:
+                raise ValueError(f"a tensor is on {t.device}, not on the current CUDA device")
+
+
 def w4_format(group: int, zeros: bool, scale_dtype) -> int:
     """The format word of a 4-bit weight: group size, zero points or not, torch.bfloat16 or torch.float16 scales."""
-    import torch
+    torch = _types()
     if scale_dtype not in (torch.bfloat16, torch.float16):
         raise ValueError("scales must be bfloat16 or float16")
     return group | (MR_W4_ZEROS if zeros else 0) | (MR_W4_SCALE_F16 if scale_dtype == torch.float16 else 0)
@@ -369,7 +393,7 @@ def w4_packed_bytes(n: int, k: int, fmt: int, paired: bool = False) -> int:
 def w4_pack(q, scales, zeros, packed, paired: bool = False, stream=None) -> None:
     """packed (uint8) = the weights q[..., n, k/2] (uint8, low half first), scales[..., n, k/G] (bf16 or f16) and
     zeros[..., n, k/G] (uint8, or None) in the order mrgemv_w4 and moe_window_w4 read."""
-    import torch
+    torch = _types()
     if q.dim() not in (2, 3) or q.dtype != torch.uint8 or packed.dtype != torch.uint8:
         raise ValueError("q must be uint8 [n, k/2] or [count, n, k/2], packed uint8")
     n, k = q.shape[-2], 2 * q.shape[-1]
@@ -383,6 +407,7 @@ def w4_pack(q, scales, zeros, packed, paired: bool = False, stream=None) -> None
         if not t.is_contiguous():
             raise ValueError("q, scales, zeros and packed must be contiguous")
     fmt = w4_format(k // groups, zeros is not None, scales.dtype)
+    _here(q, scales, zeros, packed)
     st = lib.w4_pack(q.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(), packed.data_ptr(),
                      packed.numel(), count, n, k, fmt, 1 if paired else 0, _stream(stream))
     _check(st, "w4_pack")
@@ -394,6 +419,10 @@ def mrgemv_w4(A, packed, C, fmt: int, stream=None, flags: int = 0) -> None:
     mc, n, ldc = _rows(C, "C")
     if mc != m:
         raise ValueError(f"shape mismatch A{tuple(A.shape)} C{tuple(C.shape)}")
+    torch = _types()
+    if C.dtype is not torch.float32 or packed.dtype is not torch.uint8 or not packed.is_contiguous():
+        raise ValueError("C must be float32, packed a contiguous uint8 tensor")
+    _here(A, packed, C)
     st = lib.mrgemv_w4(A.data_ptr(), lda, packed.data_ptr(), packed.numel() * packed.element_size(), C.data_ptr(),
                        ldc, m, n, k, _dtype_code(A), fmt, flags, _stream(stream))
     _check(st, "mrgemv_w4")
@@ -411,6 +440,9 @@ def _window(X, ids, weights, Y):
         raise ValueError(f"shape mismatch X{tuple(X.shape)} ids{tuple(ids.shape)} Y{tuple(Y.shape)}")
     if weights.shape != ids.shape or weights.stride() != ids.stride():
         raise ValueError("weights must match ids' shape and stride")
+    torch = _types()
+    if X.dtype is not torch.bfloat16 or ids.dtype is not torch.int32 or weights.dtype is not torch.float32:
+        raise ValueError("X must be bfloat16, ids int32 and weights float32")
     return m, topk, hidden, ldx, ldr, ldy
 
 
@@ -427,6 +459,9 @@ def moe_window_bf16(X, ids, weights, Wup, Wdown, Y, workspace, expert_base: int 
     experts, _, inter = Wdown.shape
     if tuple(Wup.shape) != (experts, 2 * inter, hidden) or Wdown.shape[1] != hidden:
         raise ValueError(f"shape mismatch Wup{tuple(Wup.shape)} Wdown{tuple(Wdown.shape)}")
+    if Wup.dtype is not X.dtype or Wdown.dtype is not X.dtype:
+        raise ValueError("Wup and Wdown must be bfloat16")
+    _here(X, ids, weights, Wup, Wdown, Y, workspace)
     st = lib.moe_window_bf16(X.data_ptr(), ldx, ids.data_ptr(), weights.data_ptr(), ldr, Wup.data_ptr(), su[1], su[0],
                              Wdown.data_ptr(), sd[1], sd[0], Y.data_ptr(), ldy, m, topk, experts, hidden, inter,
                              expert_base, _dtype_code(Y), flags, workspace.data_ptr(),
@@ -438,6 +473,9 @@ def moe_window_w4(X, ids, weights, up, down, Y, workspace, experts: int, inter: 
                   flags: int = 0, stream=None) -> None:
     """moe_window_bf16 with the experts' weights packed by w4_pack (``up`` paired, ``down`` not)."""
     m, topk, hidden, ldx, ldr, ldy = _window(X, ids, weights, Y)
+    if up.dtype is not _torch.uint8 or down.dtype is not _torch.uint8 or not (up.is_contiguous() and down.is_contiguous()):
+        raise ValueError("up and down must be contiguous uint8 tensors")
+    _here(X, ids, weights, up, down, Y, workspace)
     st = lib.moe_window_w4(X.data_ptr(), ldx, ids.data_ptr(), weights.data_ptr(), ldr, up.data_ptr(),
                            up.numel() * up.element_size(), down.data_ptr(), down.numel() * down.element_size(),
                            Y.data_ptr(), ldy, m, topk, experts, hidden, inter, expert_base, fmt, _dtype_code(Y), flags,
@@ -487,6 +525,13 @@ def token_logprobs(logits, tokens=None, logprob=None, scale: float = 1.0, lse=No
             _, topk, ldo = _rows(top_idx, "top_idx")
             iptr = top_idx.data_ptr()
             vptr = None if top_logprob is None else top_logprob.data_ptr()
+    torch = _types()
+    if tptr and tokens.dtype is not torch.int32 or iptr and top_idx.dtype is not torch.int32:
+        raise ValueError("tokens and top_idx must be int32")
+    for t in (logprob, lse, entropy, top_logprob):
+        if t is not None and t.dtype is not torch.float32:
+            raise ValueError("logprob, lse, entropy and top_logprob must be float32")
+    _here(logits, tokens, logprob, lse, entropy, top_idx, top_logprob)
     st = lib.token_logprobs(logits.data_ptr(), ldl, dtype, m, n, scale, tptr, ldt, ntok, lptr, ldp, sptr, eptr, topk,
                             iptr, vptr, ldo, _stream(stream))
     _check(st, "token_logprobs")
