@@ -54,7 +54,7 @@ typedef enum mr_status {
 enum { MR_F16 = 0, MR_BF16 = 1, MR_F32 = 2 };
 
 /* Bits of the per-device error word returned by mr_poll_errors. */
-#define MR_DEVERR_GEMV_TIMEOUT   0x1u   /* mrgemv_bf16: a weight stage never arrived */
+#define MR_DEVERR_GEMV_TIMEOUT   0x1u   /* mrgemv_bf16, mrgemv_w4, moe_window_w4: a weight stage never arrived */
 #define MR_DEVERR_GEMM_TIMEOUT   0x2u   /* gemm_f16: a TMA / MMA pipeline wait ran out */
 #define MR_DEVERR_TOPK_TIMEOUT   0x4u   /* router_topk: a wait ran out */
 #define MR_DEVERR_SELFTEST       0x8u   /* mr_selftest_wait_timeout fired as intended */

