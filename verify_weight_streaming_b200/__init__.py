@@ -354,36 +354,38 @@ def mr_selftest_wait_timeout(limit_us: int, stream=None) -> None:
     _check(lib.mr_selftest_wait_timeout(limit_us, _stream(stream)), "mr_selftest_wait_timeout")
 
 
-_torch = None
+class _T:
+    """What the calls below need of torch, filled on the first of them."""
+    bf16 = f16 = f32 = i32 = u8 = device = stream = None
 
 
 def _types():
-    """torch, imported on the first call that needs its dtypes."""
-    global _torch
-    if _torch is None:
+    if _T.device is None:
         import torch
-        _torch = torch
-    return _torch
+        _T.bf16, _T.f16, _T.f32, _T.i32, _T.u8 = (torch.bfloat16, torch.float16, torch.float32, torch.int32,
+                                                  torch.uint8)
+        _T.stream, _T.device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    return _T
 
 
-def _here(*tensors) -> None:
-    """Refuses tensors that are not on the current CUDA device (None is skipped): the kernels run there."""
-    want = None
-    for t in tensors:
-        if t is not None:
-            have = t.get_device()
-            if want is None and have >= 0:
-                want = _types()._C._cuda_getDevice()
-            if have != want:
-                raise ValueError(f"a tensor is on {t.device}, not on the current CUDA device")
+def _on(stream, first, *others):
+    """The stream handle for a call on these tensors (None is skipped), which must be on the current CUDA device:
+    the kernels run there."""
+    d = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != d:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    if d < 0 or d != _T.device():
+        raise ValueError(f"the tensors are on {first.device}, not on the current CUDA device")
+    return _T.stream(d) if stream is None else _stream(stream)
 
 
 def w4_format(group: int, zeros: bool, scale_dtype) -> int:
     """The format word of a 4-bit weight: group size, zero points or not, torch.bfloat16 or torch.float16 scales."""
-    torch = _types()
-    if scale_dtype not in (torch.bfloat16, torch.float16):
+    T = _types()
+    if scale_dtype not in (T.bf16, T.f16):
         raise ValueError("scales must be bfloat16 or float16")
-    return group | (MR_W4_ZEROS if zeros else 0) | (MR_W4_SCALE_F16 if scale_dtype == torch.float16 else 0)
+    return group | (MR_W4_ZEROS if zeros else 0) | (MR_W4_SCALE_F16 if scale_dtype is T.f16 else 0)
 
 
 def w4_packed_bytes(n: int, k: int, fmt: int, paired: bool = False) -> int:
@@ -393,23 +395,23 @@ def w4_packed_bytes(n: int, k: int, fmt: int, paired: bool = False) -> int:
 def w4_pack(q, scales, zeros, packed, paired: bool = False, stream=None) -> None:
     """packed (uint8) = the weights q[..., n, k/2] (uint8, low half first), scales[..., n, k/G] (bf16 or f16) and
     zeros[..., n, k/G] (uint8, or None) in the order mrgemv_w4 and moe_window_w4 read."""
-    torch = _types()
-    if q.dim() not in (2, 3) or q.dtype != torch.uint8 or packed.dtype != torch.uint8:
+    T = _types()
+    if q.dim() not in (2, 3) or q.dtype is not T.u8 or packed.dtype is not T.u8:
         raise ValueError("q must be uint8 [n, k/2] or [count, n, k/2], packed uint8")
     n, k = q.shape[-2], 2 * q.shape[-1]
     count = q.shape[0] if q.dim() == 3 else 1
     groups = scales.shape[-1]
     if tuple(scales.shape[:-1]) != tuple(q.shape[:-1]) or groups < 1 or k % groups:
         raise ValueError("scales must be [..., n, k/G]")
-    if zeros is not None and (zeros.shape != scales.shape or zeros.dtype != torch.uint8):
+    if zeros is not None and (zeros.shape != scales.shape or zeros.dtype is not T.u8):
         raise ValueError("zeros must be uint8 of the scales' shape")
     for t in (q, scales, packed) if zeros is None else (q, scales, packed, zeros):
         if not t.is_contiguous():
             raise ValueError("q, scales, zeros and packed must be contiguous")
     fmt = w4_format(k // groups, zeros is not None, scales.dtype)
-    _here(q, scales, zeros, packed)
+    stream = _on(stream, q, scales, zeros, packed)
     st = lib.w4_pack(q.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(), packed.data_ptr(),
-                     packed.numel(), count, n, k, fmt, 1 if paired else 0, _stream(stream))
+                     packed.numel(), count, n, k, fmt, 1 if paired else 0, stream)
     _check(st, "w4_pack")
 
 
@@ -419,12 +421,12 @@ def mrgemv_w4(A, packed, C, fmt: int, stream=None, flags: int = 0) -> None:
     mc, n, ldc = _rows(C, "C")
     if mc != m:
         raise ValueError(f"shape mismatch A{tuple(A.shape)} C{tuple(C.shape)}")
-    torch = _types()
-    if C.dtype is not torch.float32 or packed.dtype is not torch.uint8 or not packed.is_contiguous():
+    T = _types()
+    if C.dtype is not T.f32 or packed.dtype is not T.u8 or not packed.is_contiguous():
         raise ValueError("C must be float32, packed a contiguous uint8 tensor")
-    _here(A, packed, C)
-    st = lib.mrgemv_w4(A.data_ptr(), lda, packed.data_ptr(), packed.numel() * packed.element_size(), C.data_ptr(),
-                       ldc, m, n, k, _dtype_code(A), fmt, flags, _stream(stream))
+    stream = _on(stream, A, packed, C)
+    st = lib.mrgemv_w4(A.data_ptr(), lda, packed.data_ptr(), packed.numel(), C.data_ptr(), ldc, m, n, k, _dtype_code(A),
+                       fmt, flags, stream)
     _check(st, "mrgemv_w4")
 
 
@@ -438,10 +440,10 @@ def _window(X, ids, weights, Y):
     my, hy, ldy = _rows(Y, "Y")
     if mi != m or my != m or hy != hidden:
         raise ValueError(f"shape mismatch X{tuple(X.shape)} ids{tuple(ids.shape)} Y{tuple(Y.shape)}")
-    if weights.shape != ids.shape or weights.stride() != ids.stride():
+    if _rows(weights, "weights") != (m, topk, ldr):
         raise ValueError("weights must match ids' shape and stride")
-    torch = _types()
-    if X.dtype is not torch.bfloat16 or ids.dtype is not torch.int32 or weights.dtype is not torch.float32:
+    T = _types()
+    if X.dtype is not T.bf16 or ids.dtype is not T.i32 or weights.dtype is not T.f32:
         raise ValueError("X must be bfloat16, ids int32 and weights float32")
     return m, topk, hidden, ldx, ldr, ldy
 
@@ -456,16 +458,15 @@ def moe_window_bf16(X, ids, weights, Wup, Wdown, Y, workspace, expert_base: int 
     su, sd = Wup.stride(), Wdown.stride()
     if len(su) != 3 or len(sd) != 3 or su[2] != 1 or sd[2] != 1:
         raise ValueError("Wup and Wdown must be 3-D tensors with unit column stride")
-    experts, _, inter = Wdown.shape
-    if tuple(Wup.shape) != (experts, 2 * inter, hidden) or Wdown.shape[1] != hidden:
+    experts, rows, inter = Wdown.shape
+    if Wup.shape != (experts, 2 * inter, hidden) or rows != hidden:
         raise ValueError(f"shape mismatch Wup{tuple(Wup.shape)} Wdown{tuple(Wdown.shape)}")
-    if Wup.dtype is not X.dtype or Wdown.dtype is not X.dtype:
+    if Wup.dtype is not _T.bf16 or Wdown.dtype is not _T.bf16:
         raise ValueError("Wup and Wdown must be bfloat16")
-    _here(X, ids, weights, Wup, Wdown, Y, workspace)
+    stream = _on(stream, X, ids, weights, Wup, Wdown, Y, workspace)
     st = lib.moe_window_bf16(X.data_ptr(), ldx, ids.data_ptr(), weights.data_ptr(), ldr, Wup.data_ptr(), su[1], su[0],
                              Wdown.data_ptr(), sd[1], sd[0], Y.data_ptr(), ldy, m, topk, experts, hidden, inter,
-                             expert_base, _dtype_code(Y), flags, workspace.data_ptr(),
-                             workspace.numel() * workspace.element_size(), _stream(stream))
+                             expert_base, _dtype_code(Y), flags, workspace.data_ptr(), workspace.nbytes, stream)
     _check(st, "moe_window_bf16")
 
 
@@ -473,13 +474,12 @@ def moe_window_w4(X, ids, weights, up, down, Y, workspace, experts: int, inter: 
                   flags: int = 0, stream=None) -> None:
     """moe_window_bf16 with the experts' weights packed by w4_pack (``up`` paired, ``down`` not)."""
     m, topk, hidden, ldx, ldr, ldy = _window(X, ids, weights, Y)
-    if up.dtype is not _torch.uint8 or down.dtype is not _torch.uint8 or not (up.is_contiguous() and down.is_contiguous()):
+    if up.dtype is not _T.u8 or down.dtype is not _T.u8 or not (up.is_contiguous() and down.is_contiguous()):
         raise ValueError("up and down must be contiguous uint8 tensors")
-    _here(X, ids, weights, up, down, Y, workspace)
-    st = lib.moe_window_w4(X.data_ptr(), ldx, ids.data_ptr(), weights.data_ptr(), ldr, up.data_ptr(),
-                           up.numel() * up.element_size(), down.data_ptr(), down.numel() * down.element_size(),
-                           Y.data_ptr(), ldy, m, topk, experts, hidden, inter, expert_base, fmt, _dtype_code(Y), flags,
-                           workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
+    stream = _on(stream, X, ids, weights, up, down, Y, workspace)
+    st = lib.moe_window_w4(X.data_ptr(), ldx, ids.data_ptr(), weights.data_ptr(), ldr, up.data_ptr(), up.numel(),
+                           down.data_ptr(), down.numel(), Y.data_ptr(), ldy, m, topk, experts, hidden, inter,
+                           expert_base, fmt, _dtype_code(Y), flags, workspace.data_ptr(), workspace.nbytes, stream)
     _check(st, "moe_window_w4")
 
 
@@ -492,6 +492,7 @@ def token_logprobs(logits, tokens=None, logprob=None, scale: float = 1.0, lse=No
     dtype = _dtype_code(logits)
     if dtype == MR_BF16 and not logits.is_floating_point():  # no raw bit patterns here
         dtype = -1
+    T = _types()
     tptr = lptr = iptr = vptr = sptr = eptr = None
     ntok = ldt = ldp = topk = ldo = 0
     if (tokens is None) != (logprob is None):
@@ -500,38 +501,40 @@ def token_logprobs(logits, tokens=None, logprob=None, scale: float = 1.0, lse=No
         shape = tokens.shape
         if len(shape) != 2 or shape[0] != m or logprob.shape != shape:
             raise ValueError("tokens and logprob must be [m, t]")
-        if shape[1]:
-            _, ntok, ldt = _rows(tokens, "tokens")
-            ldp = _rows(logprob, "logprob")[2]
+        if tokens.dtype is not T.i32 or logprob.dtype is not T.f32:
+            raise ValueError("tokens must be int32, logprob float32")
+        ntok = shape[1]
+        if ntok:
+            ldt, cols = tokens.stride()
+            ldp, cols1 = logprob.stride()
+            if cols != 1 or cols1 != 1:
+                raise ValueError("tokens and logprob must have unit column stride")
             tptr, lptr = tokens.data_ptr(), logprob.data_ptr()
     if lse is not None:
-        if lse.shape != (m,) or lse.stride(0) != 1:
-            raise ValueError("lse must be a contiguous [m] tensor")
+        if lse.shape != (m,) or lse.stride(0) != 1 or lse.dtype is not T.f32:
+            raise ValueError("lse must be a contiguous [m] float32 tensor")
         sptr = lse.data_ptr()
     if entropy is not None:
-        if entropy.shape != (m,) or entropy.stride(0) != 1:
-            raise ValueError("entropy must be a contiguous [m] tensor")
+        if entropy.shape != (m,) or entropy.stride(0) != 1 or entropy.dtype is not T.f32:
+            raise ValueError("entropy must be a contiguous [m] float32 tensor")
         eptr = entropy.data_ptr()
     if top_idx is None:
         if top_logprob is not None:
             raise ValueError("top_logprob needs top_idx")
     else:
-        shape = top_idx.shape
-        if len(shape) != 2 or shape[0] != m:
-            raise ValueError("top_idx must be [m, k]")
-        if top_logprob is not None and (top_logprob.shape != shape or top_logprob.stride() != top_idx.stride()):
-            raise ValueError("top_logprob must match top_idx's shape and stride")
-        if shape[1]:
-            _, topk, ldo = _rows(top_idx, "top_idx")
-            iptr = top_idx.data_ptr()
+        shape, st = top_idx.shape, top_idx.stride()
+        if len(shape) != 2 or shape[0] != m or top_idx.dtype is not T.i32:
+            raise ValueError("top_idx must be [m, k] int32")
+        if top_logprob is not None and (top_logprob.shape != shape or top_logprob.stride() != st
+                                        or top_logprob.dtype is not T.f32):
+            raise ValueError("top_logprob must be float32 of top_idx's shape and stride")
+        topk = shape[1]
+        if topk:
+            if st[1] != 1:
+                raise ValueError("top_idx must have unit column stride")
+            ldo, iptr = st[0], top_idx.data_ptr()
             vptr = None if top_logprob is None else top_logprob.data_ptr()
-    torch = _types()
-    if tptr and tokens.dtype is not torch.int32 or iptr and top_idx.dtype is not torch.int32:
-        raise ValueError("tokens and top_idx must be int32")
-    for t in (logprob, lse, entropy, top_logprob):
-        if t is not None and t.dtype is not torch.float32:
-            raise ValueError("logprob, lse, entropy and top_logprob must be float32")
-    _here(logits, tokens, logprob, lse, entropy, top_idx, top_logprob)
+    stream = _on(stream, logits, tokens, logprob, lse, entropy, top_idx, top_logprob)
     st = lib.token_logprobs(logits.data_ptr(), ldl, dtype, m, n, scale, tptr, ldt, ntok, lptr, ldp, sptr, eptr, topk,
-                            iptr, vptr, ldo, _stream(stream))
+                            iptr, vptr, ldo, stream)
     _check(st, "token_logprobs")

@@ -2,6 +2,7 @@
 // (mr_poll_errors) and the bounded-wait self test.
 #include "common.cuh"
 
+#include <atomic>
 #include <condition_variable>
 #include <mutex>
 
@@ -12,19 +13,20 @@ mr_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MR_OK : MR_ERR_
 namespace {
 constexpr int kMaxDevices = 64;
 std::mutex g_mutex;
-int g_sms[kMaxDevices] = {};
+std::atomic<int> g_sms[kMaxDevices];  // 0 until a device was asked; set after g_optin
 int g_optin[kMaxDevices] = {};
 
 bool query(int &dev) {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+    if (g_sms[dev].load(std::memory_order_acquire) != 0) return true;
     std::lock_guard<std::mutex> lock(g_mutex);
-    if (g_sms[dev] == 0) {
+    if (g_sms[dev].load(std::memory_order_relaxed) == 0) {
         int sms = 0, optin = 0;
         if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return false;
         if (cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
             return false;
         g_optin[dev] = optin;
-        g_sms[dev] = sms;
+        g_sms[dev].store(sms, std::memory_order_release);
     }
     return true;
 }
@@ -32,7 +34,7 @@ bool query(int &dev) {
 
 int sm_count() {
     int dev = 0;
-    return query(dev) ? g_sms[dev] : 0;
+    return query(dev) ? g_sms[dev].load(std::memory_order_relaxed) : 0;
 }
 
 int max_smem_optin() {
