@@ -105,7 +105,8 @@ def given(seed, m, n, count):
     (64, 131072, "bf16", 5, 1, 0.7), (3, 262144, "f32", 32, 4, 1.0), (5, 1, "f32", 1, 1, 1.0), (5, 1, "bf16", 1, 3, 2.0),
     (4, 7, "f16", 7, 2, 1.0), (9, 33, "bf16", 32, 1, 1.0), (7, 512, "f32", 10, 2, 1.0), (2, 2049, "bf16", 32, 256, 1.0),
     (11, 16385, "f32", 3, 0, 1.0), (2, 32768 + 9, "bf16", 31, 1, 1.5), (3, 65536 * 4 + 1, "f16", 17, 1, 0.5),
-    (2000, 40, "f32", 4, 1, 1.0), (2, 700001, "bf16", 32, 1, 1.0),
+    (2000, 40, "f32", 4, 1, 1.0), (2, 700001, "bf16", 32, 1, 1.0), (700, 9001, "bf16", 20, 1, 1.0),
+    (640, 2048, "f32", 0, 1, 1.0), (620, 140000, "f16", 3, 1, 1.0),
 ])
 def test_rows(m, n, dtype, topk, ntok, scale):
     check(logits(n, m, n, dtype), given(n + 1, m, n, ntok), topk, scale)
@@ -215,6 +216,14 @@ def test_huge_logits_do_not_overflow():
     lp, lse, ent, ti, tl = ask(x, torch.tensor([[5, 0], [4, 0]], dtype=torch.int32).cuda(), 3)
     assert np.allclose(lp[:, 0], [-np.log(2.0), 0.0], rtol=0, atol=4 * U) and (lp[:, 1] == -np.inf).all()
     assert np.allclose(ent, [np.log(2.0), 0.0], rtol=0, atol=4 * U) and list(ti[0]) == [5, 9, 0]
+
+
+def test_a_masked_token_of_the_lowest_value_keeps_its_log_probability():
+    low = torch.finfo(torch.float32).min
+    x = logits(14, 2, 2000, "f32")
+    x[:, 100:] = low
+    lp, lse, _, _, _ = ask(x, torch.tensor([[150, 3], [1999, 7]], dtype=torch.int32).cuda(), 2)
+    assert np.allclose(lp[:, 0], low, rtol=8 * U, atol=0) and np.isfinite(lp).all() and np.isfinite(lse).all()
 
 
 def test_a_row_has_the_same_bits_alone():

@@ -7,7 +7,7 @@
 // HBM-bound when there are many rows, latency-bound when there are few.  A row
 // is summed in up to 8 pieces of about 64 KB, how many by its bytes alone, and a
 // cluster of 1 to 8 CTAs takes them: one CTA a row when the rows fill the GPU,
-// more when they do not (2048 rows of 131072 bf16: 109.5 us, 90 without top-k;
+// more when they do not (2048 rows of 131072 bf16: 109.3 us, 90 without top-k;
 // one row of 131072 fp32: 6.0 us, 3.5 without).  Threads read 16 bytes a load,
 // strided by the CTA, and keep a running reference R (the largest c x log2 e so
 // far), s = sum 2^d and t = sum d 2^d with d = c x log2 e - R, all in fp32: the
@@ -23,7 +23,9 @@
 // it and then finds the vector up to which the tied value counts.  Every top-k
 // element is in such a thread and reaches that (value, vector): any other has
 // k better ones.  So only those threads' vectors are looked at again (about k
-// of 256, from cache), and the few elements found are ranked by counting.
+// of 256, from cache), and the few elements found are ranked by counting.  (Only
+// the pieces of those threads that reach it: 2048 rows of 131072 bf16 152 -> 135 us at k =
+// 20, but 109 -> 115 at k = 5, and one row 5.9 -> 6.8.)
 // (Merging sorted lists in one warp instead cost 2.7 us a call at k = 1 and 8.7
 // us at k = 32; the bisection alone 2.6 and 4.6; this 2.3 and 4.7.)
 #include "topk_core.cuh"
@@ -46,7 +48,6 @@ constexpr int kMaxTokens = kThreads;
 constexpr int kMaxPieces = 8;
 constexpr int64_t kPieceBytes = 64 * 1024;
 constexpr int kUnroll = 4;
-constexpr int kBlocksPerSm = 4;
 constexpr int kCandidates = 1024;
 constexpr float kLog2E = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 // Logits are taken as no less than this in the sums, so that a masked (-inf)
@@ -65,7 +66,7 @@ struct Params {
     int32_t *top_idx;
     float *top_logprob;
     int64_t ldo;
-    int n, ntok, K, pieces, cluster;
+    int n, ntok, K, pieces, cluster, deep;
     float scale;
 };
 
@@ -432,7 +433,10 @@ struct Result {
     float c, M, log_sum;
     float lse, entropy;
     __device__ __forceinline__ float logprob(float x) const {
-        if (!rare) return (fmaf(x, c2, -R) - log2s) * kLn2;
+        if (!rare) {
+            const float v = fmaf(x, c2, -R) - log2s;
+            return v > -INFINITY ? v * kLn2 : fmaf(x, c, -lse);  // (x log2 e alone may overflow)
+        }
         if (!(fabsf(lse) < INFINITY) && !(M > -INFINITY && M < INFINITY)) return fmaf(x, c, -lse);
         return (x - M) * c - log_sum;
     }
@@ -480,8 +484,10 @@ __device__ void rare_row(Shared &sh, const Row<DT> &row, float c, Result &r) {
     r.entropy = r.log_sum - t / s;
 }
 
-template <int DT, bool TOP>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const Params p) {
+// DEEP: the next loads are on their way while some are summed, and 4 CTAs share an
+// SM; without, 5 do.
+template <int DT, bool TOP, bool DEEP>
+__global__ void __launch_bounds__(kThreads, DEEP ? 4 : 5) logprobs_kernel(const Params p) {
     __shared__ Shared sh;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = p.cluster > 1 ? (int)cluster_rank() : 0;
@@ -521,8 +527,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
                 for (int i = 0; i < kUnroll; ++i) u[i] = row.read(v + i * kThreads);
             }
         };
-        // The next loads are on their way while these are summed.
-        if (v + kLast < end) {
+        if (!DEEP) {
+            for (; v + kLast < end; v += kStep) {
+                uint4 u[kUnroll];
+                fetch(u);
+                take<DT, kUnroll, TOP>(u, v, c2, a, best);
+            }
+        } else if (v + kLast < end) {
             uint4 u[kUnroll];
             fetch(u);
             for (v += kStep; v + kLast < end; v += kStep) {
@@ -600,6 +611,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) logprobs_kernel(const 
 
     Result out;
     out.rare = false;
+    out.c = p.scale;
     out.c2 = c2;
     out.R = a.R;
     out.log2s = log2f(a.s);
@@ -637,8 +649,11 @@ mr_status launch(const Params &p, int64_t rows, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return mr_host::cuda_status(p.K ? cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, true>, p)
-                                    : cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, false>, p));
+    if (p.deep)
+        return mr_host::cuda_status(p.K ? cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, true, true>, p)
+                                        : cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, false, true>, p));
+    return mr_host::cuda_status(p.K ? cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, true, false>, p)
+                                    : cudaLaunchKernelEx(&cfg, logprobs_kernel<DT, false, false>, p));
 }
 
 }  // namespace logprobs
@@ -680,14 +695,18 @@ extern "C" mr_status token_logprobs(const void *logits, int64_t ldl, int32_t dty
     p.pieces = 1;
     while (p.pieces < mr::logprobs::kMaxPieces && (int64_t)n * size > p.pieces * mr::logprobs::kPieceBytes)
         p.pieces *= 2;
-    // As many CTAs a row (a piece each at the most) as leave 3.5 of them to an
-    // SM, 4.5 without top-k (us at 1, 2, 4, 8 CTAs a row, top 5: 64 rows of 131072 fp32
+    // As many CTAs a row (a piece each at the most) as leave 4.5 of them to an
+    // SM, 5 without top-k (us at 1, 2, 4, 8 CTAs a row, top 5: 64 rows of 131072 fp32
     // 28.7, 18.6, 14.0, 14.7; 128 rows 31.5, 23.5, 18.6, 24.3; 256 rows of bf16 30.6, 20.9,
-    // 25.6, 25.7; 512 rows 34.3, 39.3, 46.3, 46.3; without: 306 rows of 50021 f16 12.9, 11.3,
-    // 512 rows of 131072 29.0, 30.4).
-    const int64_t most = (int64_t)mr_host::sm_count() * (topk ? 7 : 9) / 2;
+    // 25.6, 25.7; 512 rows 34.3, 39.3, 46.3, 46.3).
+    const int64_t sms = mr_host::sm_count();
     p.cluster = 1;
-    while (p.cluster < p.pieces && (int64_t)m * p.cluster * 2 <= most) p.cluster *= 2;
+    while (p.cluster < p.pieces && (int64_t)m * p.cluster * 4 <= sms * (topk ? 9 : 10)) p.cluster *= 2;
+    // Loads ahead, unless there are more CTAs than that form holds at once and a
+    // CTA's share of a row is short (us with and without, top 5: one row of 131072 fp32
+    // 6.0, 6.5; 1024 rows 100, 112; 2048 rows of bf16 109.5, 110.3; 700 rows of 50021 f16 26.4,
+    // 21.7; 306 rows of 50021 fp32 20.4, 18.3; 2048 rows of 4096 fp32 22.1, 20.1).
+    p.deep = (int64_t)m * p.cluster <= 4 * sms || (int64_t)n * size >= p.cluster * 4 * mr::logprobs::kPieceBytes;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (dtype) {
         case MR_F32: return mr::logprobs::launch<MR_F32>(p, m, s);
