@@ -120,6 +120,7 @@ def check(got, want, tol, out=torch.float32):
     (1, 1, 1, 8, 8, 0, False, "f32"), (2, 3, 5, 24, 40, 0, False, "bf16"), (3, 2, 4, 136, 264, 0, False, "f32"),
     (1, 1, 2, 32, 32, 32, True, "f32"), (16, 32, 40, 64, 96, 32, False, "f32"), (7, 6, 9, 160, 64, 32, True, "f32"),
     (12, 1, 1, 256, 2048, 0, False, "f32"), (9, 2, 3, 4096, 128, 0, False, "f32"), (16, 3, 3, 128, 2048, 128, True, "f32"),
+    (16, 8, 1500, 32, 32, 32, True, "f32"), (16, 32, 1100, 64, 40, 0, False, "f32"), (10, 2, 2, 264, 72, 0, False, "bf16"),
 ])
 @pytest.mark.parametrize("softmax", [False, True])
 def test_layer(m, topk, count, hidden, inter, group, zeros, out, softmax):
@@ -180,6 +181,18 @@ def test_rows_have_the_same_bits_alone_and_together(group):
     order = torch.from_numpy(np.random.default_rng(4).permutation(16)).cuda()
     got = ex(x[order].contiguous(), ids[order].contiguous(), wts[order].contiguous(), flags=mr.MR_MOE_SOFTMAX)
     assert np.array_equal(got.view(np.uint32), whole[order.cpu().numpy()])
+
+
+@pytest.mark.parametrize("group", [0, 64])
+def test_few_and_many_experts_give_a_row_the_same_bits(group):
+    """One row's experts are summed by four warps a tile, 16 rows' many by one."""
+    ex = Experts(45, 200, 320, 512, group)
+    x, (ids, wts) = rows(46, 16, 320), choices(47, 16, 8, 200)
+    whole = ex(x, ids, wts).view(np.uint32)
+    for r in (0, 7, 15):
+        assert np.array_equal(ex(x[r:r + 1], ids[r:r + 1], wts[r:r + 1]).view(np.uint32), whole[r:r + 1])
+    want, tol = ex.expect(x, ids, wts)
+    check(whole.view(np.float32), want, tol)
 
 
 @pytest.mark.parametrize("group", [0, 128])

@@ -55,7 +55,8 @@ def check(c, a, w, group):
     (1, 1, 32, 32, False, "bf16", "bf16"), (16, 15, 32, 32, True, "f16", "f16"), (3, 17, 160, 32, True, "bf16", "bf16"),
     (7, 33, 64, 64, False, "f16", "bf16"), (5, 600, 192, 64, True, "bf16", "f16"), (2, 16, 128, 128, False, "bf16", "f16"),
     (16, 5000, 384, 128, False, "f16", "f16"), (4, 40000, 256, 128, False, "bf16", "bf16"),
-    (1, 128, 11264, 128, False, "bf16", "bf16"),
+    (1, 128, 11264, 128, False, "bf16", "bf16"), (3, 80000, 128, 32, True, "bf16", "f16"),
+    (16, 90001, 160, 32, False, "f16", "bf16"),
 ])
 def test_product(m, n, k, group, zeros, act, scales):
     w = w4_util.weight(n * 7 + k, (), n, k, group, zeros, scales)
@@ -87,6 +88,20 @@ def test_rows_have_the_same_bits_for_every_m(act, group):
     order = np.random.default_rng(3).permutation(16)
     assert np.array_equal(product(a[order], packed, fmt, n).view(np.uint32), whole[order])
     assert np.array_equal(product(a[5:6], packed, fmt, n).view(np.uint32), whole[5:6])
+
+
+@pytest.mark.parametrize("m,k,group", [(2, 640, 128), (11, 224, 32)])
+def test_columns_have_the_same_bits_in_a_wide_and_a_narrow_weight(m, k, group):
+    """A wide weight's tiles go to one warp each, a narrow one's to four."""
+    n = 96000
+    w = w4_util.weight(61, (), n, k, group, True)
+    packed, fmt = w4_util.pack(mr, w)
+    a = acts(62, m, k)
+    wide = product(a, packed, fmt, n).view(np.uint32)
+    for first, rows in ((0, 512), (48000, 4096), (95984, 16)):
+        at = mr.w4_packed_bytes(first, k, fmt) if first else 0
+        part = packed[at:at + mr.w4_packed_bytes(rows, k, fmt)]
+        assert np.array_equal(product(a, part, fmt, rows).view(np.uint32), wide[:, first:first + rows])
 
 
 def test_strides_and_programmatic_launch():

@@ -331,7 +331,7 @@ __device__ __forceinline__ uint32_t best_word(const Best &b) { return b.vector >
 template <int DT>
 __device__ uint64_t piece_top(Shared &sh, const Row<DT> &row, int v0, int v1, int K, const Best &best, bool rare) {
     constexpr int E = Type<DT>::E;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
     if (rare) return every_key<DT>(sh, row, v0, v1, K);
     // tau: a value at least K threads' bests reach; cut: the last vector that
     // counts with exactly that value.
