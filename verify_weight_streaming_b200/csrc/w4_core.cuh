@@ -33,11 +33,7 @@ __host__ __device__ inline int block_bytes(uint32_t fmt) {
 
 // ---- asynchronous copies into the issuing lane's own bytes ----------------
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
-// 16 bytes of zeros when !valid (nothing is read then).
+// 16 bytes, or zeros when !valid (nothing is read then).
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool valid) {
     const int n = valid ? 16 : 0;
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
