@@ -92,9 +92,11 @@ __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a
 // ---- 4-bit values ---------------------------------------------------------
 
 // One word holds 8 values: nibble i is value 2i, nibble 4 + i is value 2i + 1.
-// Pair i is (q - z) of both, exact: the nibble is put into the low mantissa
-// bits of 128 (bf16) or 1024 (f16), whose spacing is 1 there, and -(128 + z)
-// or -(1024 + z) (`minus`, both halves) is added.
+// Pair i is (q - z) of both, exact: the nibble is put into the mantissa of 128
+// (bf16) or 1024 (f16) and the zero point taken off again.  bf16: the low bits,
+// whose spacing is 1, and -(128 + z) is added (`minus`, both halves).  f16 has room
+// for a second nibble above: the odd pairs become 1024 + 16 q, and a sixteenth of
+// that minus 64 + z (`minus16`), which saves two of three shifts a word.
 // `one` is 128 or 1024 in both halves, kept in a register by `magic`: with mask
 // and constant both known, the compiler emits two logic operations for the one.
 template <bool F16>
@@ -102,20 +104,31 @@ __device__ __forceinline__ uint32_t magic(uint32_t fmt) {
     return (F16 ? 0x64006400u : 0x43004300u) + (fmt >> 31);  // no format has bit 31
 }
 
-template <bool F16>
-__device__ __forceinline__ uint32_t pair(uint32_t word, int i, uint32_t one, uint32_t minus) {
-    uint32_t v, r;
-    asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(v) : "r"(word >> (4 * i)), "r"(one));
-    if constexpr (F16)
-        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(minus));
-    else
-        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0x3F803F80u), "r"(minus));
-    return r;
-}
+struct Zero {
+    uint32_t minus, minus16;
+    template <bool F16>
+    static __device__ __forceinline__ Zero of(uint32_t z) {
+        return {z * 0x00010001u + (F16 ? 0xE400E400u : 0xC300C300u), z * 0x00100010u + 0xD400D400u};
+    }
+};
 
 template <bool F16>
-__device__ __forceinline__ uint32_t minus_zero(uint32_t z) {
-    return z * 0x00010001u + (F16 ? 0xE400E400u : 0xC300C300u);
+__device__ __forceinline__ uint32_t pair(uint32_t word, int i, uint32_t one, const Zero &zero) {
+    uint32_t v, r;
+    if constexpr (F16) {
+        const uint32_t w = word >> (8 * (i / 2));
+        if (i & 1) {
+            asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0xEA;" : "=r"(v) : "r"(w), "r"(one));
+            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0x2C002C00u), "r"(zero.minus16));
+        } else {
+            asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(v) : "r"(w), "r"(one));
+            asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(zero.minus));
+        }
+    } else {
+        asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(v) : "r"(word >> (4 * i)), "r"(one));
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0x3F803F80u), "r"(zero.minus));
+    }
+    return r;
 }
 
 // A stored 16-bit scale in fp32 (exact).
@@ -185,10 +198,10 @@ __device__ __forceinline__ void consume_block(uint32_t stage, uint32_t fmt, cons
     auto scale_of = [&](int i) {  // i: half * kGroups + group
         return scale_value((uint16_t)(sw[i / 2] >> (16 * (i & 1))), sf16);
     };
-    auto zero_of = [&](int i) { return minus_zero<F16>((zw[i / 4] >> (8 * (i & 3))) & 0xFFu); };
+    auto zero_of = [&](int i) { return Zero::of<F16>((zw[i / 4] >> (8 * (i & 3))) & 0xFFu); };
 #pragma unroll
     for (int gi = 0; gi < kGroups; ++gi) {
-        uint32_t z0 = minus_zero<F16>(8u), z8 = z0;
+        Zero z0 = Zero::of<F16>(8u), z8 = z0;
         if (zeros) {
             z0 = zero_of(gi);
             z8 = zero_of(kGroups + gi);
