@@ -95,8 +95,10 @@ __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a
 // Pair i is (q - z) of both, exact: the nibble is put into the mantissa of 128
 // (bf16) or 1024 (f16) and the zero point taken off again.  bf16: the low bits,
 // whose spacing is 1, and -(128 + z) is added (`minus`, both halves).  f16 has room
-// for a second nibble above: the odd pairs become 1024 + 16 q, and a sixteenth of
-// that minus 64 + z (`minus16`), which saves two of three shifts a word.
+// for a second nibble above (UPPER): the odd pairs become 1024 + 16 q, and a sixteenth
+// of that minus 64 + z (`minus16`), which saves two of three shifts a word
+// (131072 x 2560 at m = 4, G = 128: 40.3 -> 37.6 us) but needs a second constant a group
+// (6144 x 2560 at m = 16, G = 32 with zero points: 7.4 -> 7.7), so groups of 32 go without.
 // `one` is 128 or 1024 in both halves, kept in a register by `magic`: with mask
 // and constant both known, the compiler emits two logic operations for the one.
 template <bool F16>
@@ -112,12 +114,12 @@ struct Zero {
     }
 };
 
-template <bool F16>
+template <bool F16, bool UPPER>
 __device__ __forceinline__ uint32_t pair(uint32_t word, int i, uint32_t one, const Zero &zero) {
     uint32_t v, r;
     if constexpr (F16) {
-        const uint32_t w = word >> (8 * (i / 2));
-        if (i & 1) {
+        const uint32_t w = UPPER ? word >> (8 * (i / 2)) : word >> (4 * i);
+        if (UPPER && (i & 1)) {
             asm("lop3.b32 %0, %1, 0x00F000F0, %2, 0xEA;" : "=r"(v) : "r"(w), "r"(one));
             asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(0x2C002C00u), "r"(zero.minus16));
         } else {
@@ -212,8 +214,8 @@ __device__ __forceinline__ void consume_block(uint32_t stage, uint32_t fmt, cons
             uint32_t a0[4], a8[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                a0[i] = pair<F16>(q0[j], i, one, z0);
-                a8[i] = pair<F16>(q8[j], i, one, z8);
+                a0[i] = pair<F16, (G > 32)>(q0[j], i, one, z0);
+                a8[i] = pair<F16, (G > 32)>(q8[j], i, one, z8);
             }
 #pragma unroll
             for (int c = 0; c < NT; ++c) {
