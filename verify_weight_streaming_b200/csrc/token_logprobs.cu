@@ -54,6 +54,10 @@ constexpr float kLog2E = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 // one gives d 2^d = 0 and not NaN.  A row whose largest logit is near it or
 // below is summed again, without the bound (`rare_row`).
 constexpr float kFloor = -0x1p100f;
+// How far below another a reference counts as being when sums are joined: 2^-200
+// is 0 already, and a masked warp's reference is 2^100 c2 below with thousands of
+// logits in s, where d s would overflow and 0 times it be NaN.
+constexpr float kFar = -200.0f;
 
 struct Params {
     const uint8_t *x;
@@ -234,7 +238,7 @@ __device__ __forceinline__ void take(const uint4 (&u)[U], int first, float c, Su
         }
         m = fmaxf(m, top);
     }
-    const float R = fmaxf(a.R, fmaxf(m, kFloor) * c), d0 = a.R - R, f = ex2(d0);
+    const float R = fmaxf(a.R, fmaxf(m, kFloor) * c), d0 = fmaxf(a.R - R, kFar), f = ex2(d0);
     a.t = f * fmaf(d0, a.s, a.t);
     a.s *= f;
     a.R = R;
@@ -261,7 +265,7 @@ __device__ __forceinline__ Sums warp_sums(Sums a) {
     float R = a.R;
 #pragma unroll
     for (int d = 16; d; d >>= 1) R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, d));
-    const float d0 = a.R - R, f = ex2(d0);
+    const float d0 = fmaxf(a.R - R, kFar), f = ex2(d0);
     float s = a.s * f, t = f * fmaf(d0, a.s, a.t);
 #pragma unroll
     for (int d = 16; d; d >>= 1) {
@@ -604,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 4 : 5) logprobs_kernel(const 
     Sums a = {kFloor * c2, 0.0f, 0.0f};
     for (int i = lane; i < p.pieces * kWarps; i += 32) {
         const Sums b = sh.sums[i];
-        const float R = fmaxf(a.R, b.R), da = a.R - R, db = b.R - R, fa = ex2(da), fb = ex2(db);
+        const float R = fmaxf(a.R, b.R), da = fmaxf(a.R - R, kFar), db = fmaxf(b.R - R, kFar), fa = ex2(da), fb = ex2(db);
         a = {R, a.s * fa + b.s * fb, fa * fmaf(da, a.s, a.t) + fb * fmaf(db, b.s, b.t)};
     }
     a = warp_sums(a);
