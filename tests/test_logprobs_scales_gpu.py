@@ -94,3 +94,26 @@ def test_close_logits_at_the_largest_scale():
     x[2, :] = -5.0
     x[2, 3:15] = 1.0 + steps
     check(x, [[70003], [11000], [9]], 12, 1e6)
+
+
+@pytest.mark.parametrize("dtype,scale", [("f32", 1.0), ("f32", 40.0), ("f32", 1e6), ("bf16", 1.0), ("bf16", 40.0),
+                                         ("bf16", 1e6), ("f16", 1e6)])
+def test_logits_far_from_zero(dtype, scale):
+    """Largest products from 2^23 to 2^40: one logit well above the others, two equal ones, steps, all equal, both signs."""
+    rng = np.random.default_rng(17)
+    size = 2.0 ** rng.uniform(23, 40, 120) / scale
+    size[:3] = 1.4971036e9 / scale, 1.4971036e9 * 1.0625 / scale, 1.86e9 / scale  # about 2^31 in units of log 2
+    size = size[size < (6e4 if dtype == "f16" else 1e38)]
+    n = 3001
+    x = torch.zeros((6 * len(size), n), dtype=torch.float64)
+    for i, v in enumerate(size):
+        rows = x[6 * i:6 * i + 6]
+        rows[0, 777] = v
+        rows[1, 5], rows[1, 2999] = v, v
+        rows[2] = v * (1 - torch.arange(n) / 4096.0)
+        rows[3] = -v
+        rows[4] = -2 * v
+        rows[4, 2000] = -v
+        rows[5] = -float("inf")
+        rows[5, ::700] = -v
+    check(x.to(DT[dtype]).cuda(), [[777, 5]] * len(x), 4, scale)

@@ -51,13 +51,18 @@ constexpr int kUnroll = 4;
 constexpr int kCandidates = 1024;
 constexpr float kLog2E = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 // Logits are taken as no less than this in the sums, so that a masked (-inf)
-// one gives d 2^d = 0 and not NaN.  A row whose largest logit is near it or
-// below is summed again, without the bound (`rare_row`).
+// one gives d 2^d = 0 and not NaN.
 constexpr float kFloor = -0x1p100f;
 // How far below another a reference counts as being when sums are joined: 2^-200
 // is 0 already, and a masked warp's reference is 2^100 c2 below with thousands of
 // logits in s, where d s would overflow and 0 times it be NaN.
 constexpr float kFar = -200.0f;
+// R is M c2 rounded, d = x c2 - R is not: the largest logit's d is up to half a step of R away
+// from 0, in every term alike.  Below this |R| that is 64 at most, 2^d and d 2^d are far from overflow, and
+// a term that underflows is 2^62 below the largest.  A row beyond it is summed again, M subtracted first
+// (`rare_row`); so is one whose largest logit is near kFloor, which is far beyond, and one where some
+// threads' own references lie beyond it and their sums overflowed (2^d0 = 0 then makes them NaN).
+constexpr float kWide = 0x1p31f;
 
 struct Params {
     const uint8_t *x;
@@ -460,7 +465,7 @@ __device__ float block_fold(Shared &sh, float v, F f) {
     return v;
 }
 
-// A row with a NaN or an infinity, or with no logit above -2^99: the formulas
+// A row with a NaN or an infinity, or whose largest product is beyond kWide: the formulas
 // as they stand, two more passes by the cluster's first CTA.
 template <int DT>
 __device__ void rare_row(Shared &sh, const Row<DT> &row, float c, Result &r) {
@@ -621,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 4 : 5) logprobs_kernel(const 
     out.log2s = log2f(a.s);
     out.lse = (a.R + out.log2s) * kLn2;
     out.entropy = (out.log2s - a.t / a.s) * kLn2;
-    const bool fine = a.s > 0.0f && a.s < INFINITY && a.R > 0.5f * kFloor * c2 && a.R < INFINITY;
+    const bool fine = a.s > 0.0f && a.s < INFINITY && fabsf(a.t) < INFINITY && fabsf(a.R) < kWide;
     if (!fine) rare_row<DT>(sh, row, p.scale, out);
     if ((int)threadIdx.x < p.ntok) p.logprob[r * p.ldp + threadIdx.x] = out.logprob(given);
     if (threadIdx.x == 0) {
