@@ -73,7 +73,11 @@ enum { MR_F16 = 0, MR_BF16 = 1, MR_F32 = 2 };
  * streaming its weight into shared memory BEFORE the previous kernel on the
  * stream has finished, and waits for that kernel only before it reads A.
  * Use it only when the weight is not written by the kernel just before on the
- * same stream (static weights are the normal case); A and C keep ordinary
+ * same stream (static weights are the normal case), nor by the one before a run
+ * of kernels that let their successor start before their own predecessor has
+ * completed: cast_f32_bf16, router_topk, router_topk_ex, router_topk_merge, and
+ * mrgemv_bf16_ex and router_gemv_topk with this flag.  (The other calls of this
+ * library, and ordinary kernels, end such a run.)  A and C keep ordinary
  * stream order.  Outputs are bitwise identical with and without the flag.
  */
 
@@ -348,7 +352,8 @@ mr_status w4_pack(const void *q, const void *scales, const void *zeros, void *pa
  * C      : m rows of n fp32, row stride ldc (>= n), device (written).
  * 1 <= m <= 16; lda % 8 == 0; A and packed 16-byte aligned.  A is held in
  * shared memory: k <= 4096 is always accepted, more where m rows of it fit
- * (MR_ERR_UNSUPPORTED otherwise).  flags: 0 or MR_GEMV_PDL.
+ * (MR_ERR_UNSUPPORTED otherwise).  flags: 0 or MR_GEMV_PDL (`packed` is the
+ * weight that must not have been written just before).
  * Sums are fp32: groups on the tensor core, their scaled sums in k order.  Row
  * i's result is bitwise identical for every m and every position of the row.
  */
