@@ -742,7 +742,8 @@ extern "C" mr_status moe_window_w4(const void *X, int64_t ldx, const int32_t *id
                                    int64_t ldy, int32_t m, int32_t topk, int32_t experts, int32_t hidden,
                                    int32_t inter, int32_t expert_base, uint32_t fmt, int32_t out_dtype,
                                    uint32_t flags, void *workspace, size_t workspace_bytes, void *stream) {
-    if (inter > (1 << 30)) return MR_ERR_UNSUPPORTED;
+    if (inter < 1) return MR_ERR_INVALID_ARG;
+    if (inter > mr::moe::kMaxSize) return MR_ERR_UNSUPPORTED;  // before it is doubled
     mr_status st = mr::w4::check_format(2 * inter, hidden, fmt);
     if (st == MR_OK) st = mr::w4::check_format(hidden, inter, fmt);
     if (st != MR_OK) return st;
