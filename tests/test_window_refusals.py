@@ -17,3 +17,28 @@ def test_moe_window_w4_inter(inter, code):
     """2 * inter is formed only for sizes that hold it."""
     assert mr.lib.moe_window_w4(A, 128, A, A, 4, A, 1 << 62, A, 1 << 62, A, 128, 2, 4, 8, 128, inter, 0, 64, mr.MR_F32, 0,
                                 A, 1 << 62, None) == code
+
+
+def moe_args(torch, workspace):
+    bf = torch.bfloat16
+    return dict(X=torch.zeros(2, 128, dtype=bf), ids=torch.zeros(2, 4, dtype=torch.int32), weights=torch.zeros(2, 4),
+                Wup=torch.zeros(8, 128, 128, dtype=bf), Wdown=torch.zeros(8, 128, 64, dtype=bf), Y=torch.zeros(2, 128),
+                workspace=workspace)
+
+
+def scattered(torch, size):
+    """Workspaces that count more bytes than lie behind their address, or other ones."""
+    return (torch.zeros(2 * size, dtype=torch.uint8)[::2], torch.zeros(1, dtype=torch.uint8).expand(size),
+            torch.zeros((256, -(-size // 256)), dtype=torch.uint8).t())
+
+
+def test_moe_window_refuses_a_scattered_workspace():
+    torch = pytest.importorskip("torch")
+    for ws in scattered(torch, mr.moe_window_workspace_bytes(2, 4, 128, 64)):
+        args = moe_args(torch, ws)
+        with pytest.raises(ValueError, match="workspace"):
+            mr.moe_window_bf16(**args)
+        del args["Wup"], args["Wdown"]
+        packed = torch.zeros(8 * mr.w4_packed_bytes(128, 128, 64, True), dtype=torch.uint8)
+        with pytest.raises(ValueError, match="workspace"):
+            mr.moe_window_w4(up=packed, down=packed, experts=8, inter=64, fmt=64, **args)

@@ -434,7 +434,7 @@ def moe_window_workspace_bytes(m: int, topk: int, hidden: int, inter: int) -> in
     return int(lib.moe_window_workspace_bytes(m, topk, hidden, inter))
 
 
-def _window(X, ids, weights, Y):
+def _window(X, ids, weights, Y, workspace):
     m, hidden, ldx = _rows(X, "X")
     mi, topk, ldr = _rows(ids, "ids")
     my, hy, ldy = _rows(Y, "Y")
@@ -445,6 +445,8 @@ def _window(X, ids, weights, Y):
     T = _types()
     if X.dtype is not T.bf16 or ids.dtype is not T.i32 or weights.dtype is not T.f32:
         raise ValueError("X must be bfloat16, ids int32 and weights float32")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     return m, topk, hidden, ldx, ldr, ldy
 
 
@@ -452,9 +454,9 @@ def moe_window_bf16(X, ids, weights, Wup, Wdown, Y, workspace, expert_base: int 
                     stream=None) -> None:
     """Y[m,hidden] (fp32 or bf16) = the experts ids[m,topk] (int32) of X[m,hidden] (bf16), weighted by
     weights[m,topk] (fp32; their softmax with MR_MOE_SOFTMAX).  Wup[experts,2*inter,hidden] holds the gate rows
-    before the up rows, Wdown is [experts,hidden,inter].  ``workspace``: a CUDA tensor of at least
+    before the up rows, Wdown is [experts,hidden,inter].  ``workspace``: a contiguous CUDA tensor of at least
     moe_window_workspace_bytes(...) bytes."""
-    m, topk, hidden, ldx, ldr, ldy = _window(X, ids, weights, Y)
+    m, topk, hidden, ldx, ldr, ldy = _window(X, ids, weights, Y, workspace)
     su, sd = Wup.stride(), Wdown.stride()
     if len(su) != 3 or len(sd) != 3 or su[2] != 1 or sd[2] != 1:
         raise ValueError("Wup and Wdown must be 3-D tensors with unit column stride")
@@ -473,7 +475,7 @@ def moe_window_bf16(X, ids, weights, Wup, Wdown, Y, workspace, expert_base: int 
 def moe_window_w4(X, ids, weights, up, down, Y, workspace, experts: int, inter: int, fmt: int, expert_base: int = 0,
                   flags: int = 0, stream=None) -> None:
     """moe_window_bf16 with the experts' weights packed by w4_pack (``up`` paired, ``down`` not)."""
-    m, topk, hidden, ldx, ldr, ldy = _window(X, ids, weights, Y)
+    m, topk, hidden, ldx, ldr, ldy = _window(X, ids, weights, Y, workspace)
     if up.dtype is not _T.u8 or down.dtype is not _T.u8 or not (up.is_contiguous() and down.is_contiguous()):
         raise ValueError("up and down must be contiguous uint8 tensors")
     stream = _on(stream, X, ids, weights, up, down, Y, workspace)
