@@ -42,3 +42,12 @@ def test_moe_window_refuses_a_scattered_workspace():
         packed = torch.zeros(8 * mr.w4_packed_bytes(128, 128, 64, True), dtype=torch.uint8)
         with pytest.raises(ValueError, match="workspace"):
             mr.moe_window_w4(up=packed, down=packed, experts=8, inter=64, fmt=64, **args)
+
+
+def test_router_refuses_a_scattered_workspace():
+    torch = pytest.importorskip("torch")
+    bf = torch.bfloat16
+    for ws in scattered(torch, mr.router_gemv_topk_workspace_bytes(2, 64, False)):
+        with pytest.raises(ValueError, match="workspace"):
+            mr.router_gemv_topk(torch.zeros(2, 128, dtype=bf), torch.zeros(64, 128, dtype=bf), 4,
+                                torch.zeros(2, 4, dtype=torch.int32), workspace=ws, stream=0)

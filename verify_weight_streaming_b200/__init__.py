@@ -252,7 +252,7 @@ def router_gemv_topk_workspace_bytes(m: int, n: int, logits_provided: bool) -> i
 def router_gemv_topk(A, Wt, topk: int, idx, val=None, logits=None, workspace=None, stream=None,
                      flags: int = 0) -> None:
     """GEMV + per-row top-k in one launch (or, with MR_ROUTER_TWO_LAUNCH, the
-    GEMV kernel then the top-k kernel).  ``workspace``: a zeroed CUDA tensor
+    GEMV kernel then the top-k kernel).  ``workspace``: a zeroed contiguous CUDA tensor
     of at least router_gemv_topk_workspace_bytes(...) bytes (each fused call
     leaves its tag array zero again)."""
     m, k, lda = _rows(A, "A")
@@ -276,6 +276,8 @@ def router_gemv_topk(A, Wt, topk: int, idx, val=None, logits=None, workspace=Non
         vptr = val.data_ptr()
     if workspace is None:
         raise ValueError("router_gemv_topk needs a zero-initialised workspace tensor")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     wbytes = workspace.numel() * workspace.element_size()
     st = lib.router_gemv_topk(A.data_ptr(), lda, Wt.data_ptr(), ldw, lptr, ldl, m, n, k, topk,
                               idx.data_ptr(), vptr, ldo, workspace.data_ptr(), wbytes, flags,
