@@ -51,3 +51,24 @@ def test_router_refuses_a_scattered_workspace():
         with pytest.raises(ValueError, match="workspace"):
             mr.router_gemv_topk(torch.zeros(2, 128, dtype=bf), torch.zeros(64, 128, dtype=bf), 4,
                                 torch.zeros(2, 4, dtype=torch.int32), workspace=ws, stream=0)
+
+
+@pytest.mark.parametrize("group", [256, 288, 320, 384, 640, 896, 1024 + 128, 2 ** 16 + 64, -128, -1])
+def test_group_sizes_that_no_format_word_holds(group):
+    """Added to the flag bits they would be another format: 384 = 128 with zero points, 640 = 128 with f16 scales."""
+    torch = pytest.importorskip("torch")
+    for zeros in (False, True):
+        for dtype in (torch.bfloat16, torch.float16):
+            with pytest.raises(ValueError, match="group"):
+                mr.w4_format(group, zeros, dtype)
+
+
+def test_pack_refuses_one_group_a_row_that_is_too_long():
+    """The scales of a 384-long group would be read as three groups' of 128, past their end."""
+    torch = pytest.importorskip("torch")
+    for k, dtype, zeros in ((384, torch.bfloat16, True), (640, torch.float16, False), (288, torch.bfloat16, True),
+                            (896, torch.float16, True)):
+        q, s = torch.zeros(16, k // 2, dtype=torch.uint8), torch.zeros(16, 1, dtype=dtype)
+        z = torch.zeros(16, 1, dtype=torch.uint8) if zeros else None
+        with pytest.raises(ValueError, match="group"):
+            mr.w4_pack(q, s, z, torch.zeros(1 << 16, dtype=torch.uint8))

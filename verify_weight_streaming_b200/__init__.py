@@ -387,6 +387,8 @@ def w4_format(group: int, zeros: bool, scale_dtype) -> int:
     T = _types()
     if scale_dtype not in (T.bf16, T.f16):
         raise ValueError("scales must be bfloat16 or float16")
+    if not 0 <= group <= MR_W4_GROUP_MASK:  # beyond it the group would run into the flags
+        raise ValueError(f"a group of {group} values does not fit a format word")
     return group | (MR_W4_ZEROS if zeros else 0) | (MR_W4_SCALE_F16 if scale_dtype is T.f16 else 0)
 
 
