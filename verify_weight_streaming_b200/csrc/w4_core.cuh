@@ -299,7 +299,7 @@ struct Ring {
     int slots, stage_bytes;
     int put_at = 0, take_at = 0;
     uint32_t parity = 0;
-    bool dead = false;  // a wait ran out: later ones are not tried
+    bool dead = false;  // a wait ran out: no more are tried, and nothing more is requested
     __device__ __forceinline__ Ring(uint32_t d, uint32_t b, int n, int bytes)
         : data(d), bars(b), slots(n), stage_bytes(bytes) {}
     __device__ __forceinline__ void init(int lane) const {
@@ -310,15 +310,32 @@ struct Ring {
         __syncwarp();
     }
     __device__ __forceinline__ void request(const uint8_t *src, int bytes, int lane) {
-        if (lane == 0) {
+        if (lane == 0 && !dead) {
             mbar_arrive_expect_tx(bars + 8 * put_at, (uint32_t)bytes);
             bulk_g2s(data + put_at * stage_bytes, src, (uint32_t)bytes, bars + 8 * put_at);
         }
         put_at = put_at + 1 == slots ? 0 : put_at + 1;
     }
     __device__ __forceinline__ uint32_t wait() {  // the next stage, once its bytes have arrived
-        if (!dead) dead = !mbar_wait_bounded(bars + 8 * take_at, parity, MR_DEVERR_GEMV_TIMEOUT);
+        if (!dead && !mbar_wait_bounded(bars + 8 * take_at, parity, MR_DEVERR_GEMV_TIMEOUT)) {
+            dead = true;
+            drain();
+        }
         return data + take_at * stage_bytes;
+    }
+    // After a wait that ran out: a bounded one for each copy on its way, this one's too, so that
+    // none lands in shared memory that the CTA has left.
+    __device__ __forceinline__ void drain() const {
+        int at = take_at, count = put_at > take_at ? put_at - take_at : put_at - take_at + slots;
+        uint32_t phase = parity;
+#pragma unroll 1
+        for (; count > 0; --count) {
+            mbar_wait_bounded(bars + 8 * at, phase, MR_DEVERR_GEMV_TIMEOUT);
+            if (++at == slots) {
+                at = 0;
+                phase ^= 1u;
+            }
+        }
     }
     __device__ __forceinline__ void done() {  // this lane has read the stage
         __syncwarp();
