@@ -15,7 +15,8 @@ better), the per-m curve (us_per_row, GB/s, the batching speedup
 us_per_row(1)/us_per_row(8)), the GEMV roofline against the measured HBM copy
 bandwidth, an end-to-end number through the public API with host buffers, the
 GEMM TFLOP/s sweep on the prompt-chunk shapes, the CPU oracle as a baseline,
-and the SM clocks seen during the timed region.
+and the SM clocks seen during the timed region.  The full tables behind the
+curve, the GEMM sweep and the path sweep go to stderr, as one JSON line too.
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--impl reference]
     python bench.py --profile-case gemv|topk|gemm|...   # a few launches, for ncu
@@ -47,6 +48,27 @@ FALLBACK_BF16_TFLOPS = 1590.0
 def roofline_time_us(nbytes: float, gbps: float) -> float:
     """Time in microseconds to move ``nbytes`` at ``gbps`` GB/s (1 GB = 1e9 B)."""
     return nbytes / (gbps * 1e9) * 1e6
+
+
+def short_line(line: dict) -> dict:
+    """The line as it is printed: seven digits, and of the three tables one figure an entry
+    (whole they make it 26 KB, more than a log's tail keeps)."""
+    def digits(x):
+        if isinstance(x, float):
+            return float(f"{x:.7g}")
+        if isinstance(x, dict):
+            return {k: digits(v) for k, v in x.items()}
+        return [digits(v) for v in x] if isinstance(x, list) else x
+
+    out = dict(line)
+    out["curve"] = {name: {m: e["us_per_row"] if isinstance(e, dict) else e for m, e in rows.items()}
+                    if isinstance(rows, dict) else rows for name, rows in line["curve"].items()}
+    if line["gemm"]:
+        out["gemm"] = {"chunk": {shape: e["TFLOPs"] for shape, e in line["gemm"]["chunk"].items()},
+                       "summary": line["gemm"]["summary"]}
+    if line["path_sweep"]:
+        out["path_sweep"] = {name: e["crossover_m"] for name, e in line["path_sweep"].items()}
+    return digits(out)
 
 
 def gemv_bytes(m: int, n: int, k: int) -> int:
@@ -451,7 +473,8 @@ def run_gpu(args, world, rank, local):
             "e2e": e2e, "gemm": gemm, "path_sweep": sweep, "cpu_baseline": cpu, "cpu_baselines": cpus,
             "pdl": not args.no_pdl,
         }
-        print(json.dumps(line), flush=True)
+        print(json.dumps({"tables": {k: line[k] for k in ("curve", "gemm", "path_sweep")}}), file=sys.stderr, flush=True)
+        print(json.dumps(short_line(line)), flush=True)
     if world > 1:
         dist.destroy_process_group()
 
