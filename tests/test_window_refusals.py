@@ -72,3 +72,36 @@ def test_pack_refuses_one_group_a_row_that_is_too_long():
         z = torch.zeros(16, 1, dtype=torch.uint8) if zeros else None
         with pytest.raises(ValueError, match="group"):
             mr.w4_pack(q, s, z, torch.zeros(1 << 16, dtype=torch.uint8))
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """The C entry points take int32: a larger size must not be cut to its low bits."""
+    torch = pytest.importorskip("torch")
+    new = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device="meta")  # noqa: E731
+    wide, bf, i32, u8 = 2 ** 32 + 5, torch.bfloat16, torch.int32, torch.uint8
+    with pytest.raises(ValueError, match="32 bits"):
+        mr.token_logprobs(new(1, wide), lse=new(1))
+    with pytest.raises(ValueError, match="32 bits"):
+        mr.token_logprobs(new(wide, 4), lse=new(wide))
+    with pytest.raises(ValueError, match="32 bits"):
+        mr.token_logprobs(new(1, 8), new(1, wide, dtype=i32), new(1, wide))
+    with pytest.raises(ValueError, match="32 bits"):
+        mr.mrgemv_w4(new(2, 128, dtype=bf), new(1 << 20, dtype=u8), new(2, wide), 128)
+    with pytest.raises(ValueError, match="32 bits"):
+        mr.mrgemv_w4(new(2 ** 32 + 2, 128, dtype=bf), new(1 << 20, dtype=u8), new(2 ** 32 + 2, 16), 128)
+    with pytest.raises(ValueError, match="32 bits"):
+        mr.w4_pack(new(2 ** 32 + 16, 64, dtype=u8), new(2 ** 32 + 16, 1, dtype=bf), None, new(1 << 20, dtype=u8))
+    with pytest.raises(ValueError, match="32 bits"):
+        mr.w4_pack(new(2 ** 32 + 1, 16, 64, dtype=u8), new(2 ** 32 + 1, 16, 1, dtype=bf), None, new(1 << 20, dtype=u8))
+    args = moe_args(torch, torch.zeros(1 << 16, dtype=u8))
+    for size in (lambda: mr.w4_packed_bytes(2 ** 32 + 16, 128, 128), lambda: mr.moe_window_workspace_bytes(1, 1, 2 ** 32 + 8, 8)):
+        with pytest.raises(ValueError, match="32 bits"):
+            size()
+    for base in (2 ** 32, 2 ** 31, -(2 ** 32)):
+        with pytest.raises(ValueError, match="32 bits"):
+            mr.moe_window_bf16(expert_base=base, **args)
+    del args["Wup"], args["Wdown"]
+    packed = torch.zeros(1 << 20, dtype=u8)
+    for bad in (dict(experts=2 ** 32 + 8), dict(inter=2 ** 32 + 64), dict(expert_base=2 ** 32)):
+        with pytest.raises(ValueError, match="32 bits"):
+            mr.moe_window_w4(up=packed, down=packed, fmt=64, **dict(dict(experts=8, inter=64), **bad), **args)

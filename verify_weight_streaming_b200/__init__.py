@@ -382,6 +382,12 @@ def _on(stream, first, *others):
     return _T.stream(d) if stream is None else _stream(stream)
 
 
+def _int32(*sizes):
+    """The C entry points take int32, and ctypes would cut a larger size to its low bits."""
+    if max(sizes) > 0x7FFFFFFF or min(sizes) < -0x80000000:
+        raise ValueError(f"a size of {sizes} is beyond 32 bits")
+
+
 def w4_format(group: int, zeros: bool, scale_dtype) -> int:
     """The format word of a 4-bit weight: group size, zero points or not, torch.bfloat16 or torch.float16 scales."""
     T = _types()
@@ -393,6 +399,7 @@ def w4_format(group: int, zeros: bool, scale_dtype) -> int:
 
 
 def w4_packed_bytes(n: int, k: int, fmt: int, paired: bool = False) -> int:
+    _int32(n, k)
     return int(lib.w4_packed_bytes(n, k, fmt, 1 if paired else 0))
 
 
@@ -405,6 +412,7 @@ def w4_pack(q, scales, zeros, packed, paired: bool = False, stream=None) -> None
     n, k = q.shape[-2], 2 * q.shape[-1]
     count = q.shape[0] if q.dim() == 3 else 1
     groups = scales.shape[-1]
+    _int32(count, n, k)
     if tuple(scales.shape[:-1]) != tuple(q.shape[:-1]) or groups < 1 or k % groups:
         raise ValueError("scales must be [..., n, k/G]")
     if zeros is not None and (zeros.shape != scales.shape or zeros.dtype is not T.u8):
@@ -425,6 +433,8 @@ def mrgemv_w4(A, packed, C, fmt: int, stream=None, flags: int = 0) -> None:
     mc, n, ldc = _rows(C, "C")
     if mc != m:
         raise ValueError(f"shape mismatch A{tuple(A.shape)} C{tuple(C.shape)}")
+    if (m | n | k) >> 31:
+        _int32(m, n, k)
     T = _types()
     if C.dtype is not T.f32 or packed.dtype is not T.u8 or not packed.is_contiguous():
         raise ValueError("C must be float32, packed a contiguous uint8 tensor")
@@ -435,6 +445,7 @@ def mrgemv_w4(A, packed, C, fmt: int, stream=None, flags: int = 0) -> None:
 
 
 def moe_window_workspace_bytes(m: int, topk: int, hidden: int, inter: int) -> int:
+    _int32(m, topk, hidden, inter)
     return int(lib.moe_window_workspace_bytes(m, topk, hidden, inter))
 
 
@@ -451,6 +462,7 @@ def _window(X, ids, weights, Y, workspace):
         raise ValueError("X must be bfloat16, ids int32 and weights float32")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
+    _int32(m, topk, hidden)
     return m, topk, hidden, ldx, ldr, ldy
 
 
@@ -469,6 +481,7 @@ def moe_window_bf16(X, ids, weights, Wup, Wdown, Y, workspace, expert_base: int 
         raise ValueError(f"shape mismatch Wup{tuple(Wup.shape)} Wdown{tuple(Wdown.shape)}")
     if Wup.dtype is not _T.bf16 or Wdown.dtype is not _T.bf16:
         raise ValueError("Wup and Wdown must be bfloat16")
+    _int32(experts, inter, expert_base)
     stream = _on(stream, X, ids, weights, Wup, Wdown, Y, workspace)
     st = lib.moe_window_bf16(X.data_ptr(), ldx, ids.data_ptr(), weights.data_ptr(), ldr, Wup.data_ptr(), su[1], su[0],
                              Wdown.data_ptr(), sd[1], sd[0], Y.data_ptr(), ldy, m, topk, experts, hidden, inter,
@@ -482,6 +495,7 @@ def moe_window_w4(X, ids, weights, up, down, Y, workspace, experts: int, inter: 
     m, topk, hidden, ldx, ldr, ldy = _window(X, ids, weights, Y, workspace)
     if up.dtype is not _T.u8 or down.dtype is not _T.u8 or not (up.is_contiguous() and down.is_contiguous()):
         raise ValueError("up and down must be contiguous uint8 tensors")
+    _int32(experts, inter, expert_base)
     stream = _on(stream, X, ids, weights, up, down, Y, workspace)
     st = lib.moe_window_w4(X.data_ptr(), ldx, ids.data_ptr(), weights.data_ptr(), ldr, up.data_ptr(), up.numel(),
                            down.data_ptr(), down.numel(), Y.data_ptr(), ldy, m, topk, experts, hidden, inter,
@@ -540,6 +554,8 @@ def token_logprobs(logits, tokens=None, logprob=None, scale: float = 1.0, lse=No
                 raise ValueError("top_idx must have unit column stride")
             ldo, iptr = st[0], top_idx.data_ptr()
             vptr = None if top_logprob is None else top_logprob.data_ptr()
+    if (m | n | ntok | topk) >> 31:
+        _int32(m, n, ntok, topk)
     stream = _on(stream, logits, tokens, logprob, lse, entropy, top_idx, top_logprob)
     st = lib.token_logprobs(logits.data_ptr(), ldl, dtype, m, n, scale, tptr, ldt, ntok, lptr, ldp, sptr, eptr, topk,
                             iptr, vptr, ldo, stream)
