@@ -382,6 +382,14 @@ def _on(stream, first, *others):
     return _T.stream(d) if stream is None else _stream(stream)
 
 
+def _matrix(t, name):
+    """_rows, where the stride of a dimension of size one may be anything."""
+    st, sh = t.stride(), t.shape
+    if len(sh) != 2 or (st[1] != 1 and sh[1] != 1):
+        raise ValueError(f"{name} must be a 2-D tensor with unit column stride")
+    return sh[0], sh[1], st[0] if sh[0] > 1 else sh[1]
+
+
 def _int32(*sizes):
     """The C entry points take int32, and ctypes would cut a larger size to its low bits."""
     if max(sizes) > 0x7FFFFFFF or min(sizes) < -0x80000000:
@@ -429,8 +437,8 @@ def w4_pack(q, scales, zeros, packed, paired: bool = False, stream=None) -> None
 
 def mrgemv_w4(A, packed, C, fmt: int, stream=None, flags: int = 0) -> None:
     """C[m,n] (fp32) = A[m,k] (bf16 or f16) . (the packed 4-bit n x k weight)^T; m <= 16."""
-    m, k, lda = _rows(A, "A")
-    mc, n, ldc = _rows(C, "C")
+    m, k, lda = _matrix(A, "A")
+    mc, n, ldc = _matrix(C, "C")
     if mc != m:
         raise ValueError(f"shape mismatch A{tuple(A.shape)} C{tuple(C.shape)}")
     if (m | n | k) >> 31:
@@ -450,12 +458,12 @@ def moe_window_workspace_bytes(m: int, topk: int, hidden: int, inter: int) -> in
 
 
 def _window(X, ids, weights, Y, workspace):
-    m, hidden, ldx = _rows(X, "X")
-    mi, topk, ldr = _rows(ids, "ids")
-    my, hy, ldy = _rows(Y, "Y")
+    m, hidden, ldx = _matrix(X, "X")
+    mi, topk, ldr = _matrix(ids, "ids")
+    my, hy, ldy = _matrix(Y, "Y")
     if mi != m or my != m or hy != hidden:
         raise ValueError(f"shape mismatch X{tuple(X.shape)} ids{tuple(ids.shape)} Y{tuple(Y.shape)}")
-    if _rows(weights, "weights") != (m, topk, ldr):
+    if _matrix(weights, "weights") != (m, topk, ldr):
         raise ValueError("weights must match ids' shape and stride")
     T = _types()
     if X.dtype is not T.bf16 or ids.dtype is not T.i32 or weights.dtype is not T.f32:
@@ -483,8 +491,9 @@ def moe_window_bf16(X, ids, weights, Wup, Wdown, Y, workspace, expert_base: int 
         raise ValueError("Wup and Wdown must be bfloat16")
     _int32(experts, inter, expert_base)
     stream = _on(stream, X, ids, weights, Wup, Wdown, Y, workspace)
-    st = lib.moe_window_bf16(X.data_ptr(), ldx, ids.data_ptr(), weights.data_ptr(), ldr, Wup.data_ptr(), su[1], su[0],
-                             Wdown.data_ptr(), sd[1], sd[0], Y.data_ptr(), ldy, m, topk, experts, hidden, inter,
+    eu, ed = (su[0], sd[0]) if experts > 1 else (0, 0)
+    st = lib.moe_window_bf16(X.data_ptr(), ldx, ids.data_ptr(), weights.data_ptr(), ldr, Wup.data_ptr(), su[1], eu,
+                             Wdown.data_ptr(), sd[1], ed, Y.data_ptr(), ldy, m, topk, experts, hidden, inter,
                              expert_base, _dtype_code(Y), flags, workspace.data_ptr(), workspace.nbytes, stream)
     _check(st, "moe_window_bf16")
 
@@ -508,7 +517,7 @@ def token_logprobs(logits, tokens=None, logprob=None, scale: float = 1.0, lse=No
     """Log probabilities (fp32) of logits[m,n] (fp32, bf16 or f16) times ``scale``, into whichever outputs are given:
     logprob[m,t] of tokens[m,t] (int32), lse[m], entropy[m], and the top_idx.shape[1] best alternatives
     top_idx[m,k] (int32), top_logprob[m,k]."""
-    m, n, ldl = _rows(logits, "logits")
+    m, n, ldl = _matrix(logits, "logits")
     dtype = _dtype_code(logits)
     if dtype == MR_BF16 and not logits.is_floating_point():  # no raw bit patterns here
         dtype = -1
@@ -527,33 +536,41 @@ def token_logprobs(logits, tokens=None, logprob=None, scale: float = 1.0, lse=No
         if ntok:
             ldt, cols = tokens.stride()
             ldp, cols1 = logprob.stride()
-            if cols != 1 or cols1 != 1:
+            if (cols != 1 or cols1 != 1) and ntok != 1:
                 raise ValueError("tokens and logprob must have unit column stride")
+            if m == 1:  # strides of dimensions of size one may be anything
+                ldt = ldp = ntok
             tptr, lptr = tokens.data_ptr(), logprob.data_ptr()
     if lse is not None:
-        if lse.shape != (m,) or lse.stride(0) != 1 or lse.dtype is not T.f32:
+        if lse.shape != (m,) or (lse.stride(0) != 1 and m != 1) or lse.dtype is not T.f32:
             raise ValueError("lse must be a contiguous [m] float32 tensor")
         sptr = lse.data_ptr()
     if entropy is not None:
-        if entropy.shape != (m,) or entropy.stride(0) != 1 or entropy.dtype is not T.f32:
+        if entropy.shape != (m,) or (entropy.stride(0) != 1 and m != 1) or entropy.dtype is not T.f32:
             raise ValueError("entropy must be a contiguous [m] float32 tensor")
         eptr = entropy.data_ptr()
     if top_idx is None:
         if top_logprob is not None:
             raise ValueError("top_logprob needs top_idx")
     else:
-        shape, st = top_idx.shape, top_idx.stride()
+        shape = top_idx.shape
         if len(shape) != 2 or shape[0] != m or top_idx.dtype is not T.i32:
             raise ValueError("top_idx must be [m, k] int32")
-        if top_logprob is not None and (top_logprob.shape != shape or top_logprob.stride() != st
-                                        or top_logprob.dtype is not T.f32):
-            raise ValueError("top_logprob must be float32 of top_idx's shape and stride")
+        if top_logprob is not None and (top_logprob.shape != shape or top_logprob.dtype is not T.f32):
+            raise ValueError("top_logprob must be float32 of top_idx's shape")
         topk = shape[1]
         if topk:
-            if st[1] != 1:
+            ldo, cols = top_idx.stride()
+            iptr = top_idx.data_ptr()
+            if top_logprob is not None:
+                ldv, cols1 = top_logprob.stride()
+                if (cols1 != 1 and topk != 1) or (ldv != ldo and m != 1):
+                    raise ValueError("top_logprob must have top_idx's stride")
+                vptr = top_logprob.data_ptr()
+            if cols != 1 and topk != 1:
                 raise ValueError("top_idx must have unit column stride")
-            ldo, iptr = st[0], top_idx.data_ptr()
-            vptr = None if top_logprob is None else top_logprob.data_ptr()
+            if m == 1:
+                ldo = topk
     if (m | n | ntok | topk) >> 31:
         _int32(m, n, ntok, topk)
     stream = _on(stream, logits, tokens, logprob, lse, entropy, top_idx, top_logprob)
